@@ -292,9 +292,9 @@ def work(case):
         rows = min(n, vocab)   # a row that several tokens share is read once
         return dict(bytes=n * (_BYTES[case["index"]] + width * _BYTES[case["out"]]) + rows * width * _BYTES[case["weight"]],
                     flops=n * width)
-    table = vocab * width * _BYTES[case["grad"]]
-    return dict(bytes=n * (_BYTES[case["index"]] + width * _BYTES[case["dy"]]) + (2 * table if case["add"] else table),
-                flops=n * width)
+    # added to, only the rows of the batch's tokens have to be read and written; else every row is written
+    table = (2 * min(n, vocab) if case["add"] else vocab) * width * _BYTES[case["grad"]]
+    return dict(bytes=n * (_BYTES[case["index"]] + width * _BYTES[case["dy"]]) + table, flops=n * width)
 
 
 # ------------------------------------------------------- definitions in 64 bits
