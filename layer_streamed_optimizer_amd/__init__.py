@@ -12,6 +12,10 @@ PyTorch, where used, only provides device memory and streams.
     ls = LayerStream(max_layer_bytes, max_layer_params, grad_fn, user)
     ls.stream_layers(host_layers)             # H2D / update / D2H, double-buffered
     ls.stream_files(file_layers)              # the disk tier (see disk.LayerFiles)
+
+Operators around the update (include/lso_ops.h) are in ops.py and exported
+here: orthogonalize and muon_step over tables of matrices, embed_lookup and
+embed_grad of an embedding table.
 """
 from __future__ import annotations
 
@@ -35,6 +39,9 @@ __all__ = ["BlockTable", "adam_step", "adam_step_noalloc", "adam_step_norms", "l
            "LSO_OPT_SGD", "LSO_DT_BF16", "LSO_DT_NONE", "LSO_DT_F32", "LSO_LAYOUT_PLANAR",
            "LSO_LAYOUT_TILED", "LSO_TILE_ELEMS", "BLOCK_DTYPE", "HOST_LAYER_DTYPE", "FILE_LAYER_DTYPE",
            "LSO_FILE_SYNC", "LSO_FILE_SHADOW", "LSO_SHADOW_HEADER_BYTES", "shadow_format",
+           "MatrixTable", "MuonTable", "orthogonalize", "orthogonalize_workspace_bytes", "muon_step",
+           "muon_workspace_bytes", "embed_lookup", "embed_grad", "embed_grad_workspace_bytes", "EmbedProducer", "dtype_of",
+           "LSO_DT_I32", "LSO_DT_I64", "LSO_NS_AUTO", "LSO_NS_FULL", "LSO_NS_HALF", "LSO_MUON_NESTEROV", "LSO_EMBED_ADD",
            "shadow_state", "shadow_commit", "stream_handle", "tiled_state_bytes", "tiled_pack", "tiled_unpack"]
 
 
@@ -328,3 +335,8 @@ class LayerStream:
             self.close()
         except Exception:
             pass
+
+
+from .ops import (LSO_DT_I32, LSO_DT_I64, LSO_EMBED_ADD, LSO_MUON_NESTEROV, LSO_NS_AUTO, LSO_NS_FULL,  # noqa: E402
+                  LSO_NS_HALF, EmbedProducer, MatrixTable, MuonTable, dtype_of, embed_grad, embed_grad_workspace_bytes,
+                  embed_lookup, muon_step, muon_workspace_bytes, orthogonalize, orthogonalize_workspace_bytes)

@@ -1,4 +1,4 @@
-"""ctypes view of include/lso.h (argument marshalling only).
+"""ctypes view of include/lso.h and include/lso_ops.h (argument marshalling only).
 
 Every step of the update runs in liblso.so.  If the library is missing the
 import still works (so host-side code can be inspected), but every call
@@ -97,6 +97,84 @@ class LsoFileLayer(ctypes.Structure):
     ]
 
 
+LSO_DT_I32, LSO_DT_I64 = 3, 4
+LSO_NS_AUTO, LSO_NS_FULL, LSO_NS_HALF = 0, 1, 2
+LSO_NS_SMALL_SIDE, LSO_NS_MAX_STEPS = 32, 16
+LSO_MUON_NESTEROV = 1
+LSO_EMBED_ADD = 1
+
+
+class LsoNsParams(ctypes.Structure):
+    _fields_ = [
+        ("steps", ctypes.c_uint32),
+        ("precision", ctypes.c_uint32),
+        ("eps", ctypes.c_double),
+        ("coef", ctypes.c_void_p),
+    ]
+
+
+class LsoMatrix(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("rows", ctypes.c_uint64),
+        ("cols", ctypes.c_uint64),
+        ("ld_x", ctypes.c_uint64),
+        ("ld_y", ctypes.c_uint64),
+        ("x_dtype", ctypes.c_uint32),
+        ("y_dtype", ctypes.c_uint32),
+    ]
+
+
+class LsoMuonBlock(ctypes.Structure):
+    _fields_ = [
+        ("base", ctypes.c_void_p),
+        ("rows", ctypes.c_uint64),
+        ("cols", ctypes.c_uint64),
+        ("off_master", ctypes.c_uint64),
+        ("off_m", ctypes.c_uint64),
+        ("off_grad", ctypes.c_uint64),
+        ("off_weight", ctypes.c_uint64),
+        ("grad_dtype", ctypes.c_uint32),
+        ("weight_dtype", ctypes.c_uint32),
+        ("flags", ctypes.c_uint32),
+        ("reserved", ctypes.c_uint32),
+        ("lr", ctypes.c_double),
+        ("beta", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+        ("scale", ctypes.c_double),
+    ]
+
+
+class LsoEmbed(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_void_p),
+        ("n", ctypes.c_uint64),
+        ("table", ctypes.c_void_p),
+        ("vocab", ctypes.c_uint64),
+        ("width", ctypes.c_uint64),
+        ("ld_table", ctypes.c_uint64),
+        ("rows", ctypes.c_void_p),
+        ("ld_rows", ctypes.c_uint64),
+        ("token_dtype", ctypes.c_uint32),
+        ("table_dtype", ctypes.c_uint32),
+        ("rows_dtype", ctypes.c_uint32),
+        ("flags", ctypes.c_uint32),
+        ("scale", ctypes.c_double),
+    ]
+
+
+class LsoEmbedProducerArgs(ctypes.Structure):
+    _fields_ = [
+        ("grad", LsoEmbed),
+        ("embed_layer", ctypes.c_size_t),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_uint64),
+        ("other", ctypes.c_void_p),
+        ("other_user", ctypes.c_void_p),
+    ]
+
+
 GRAD_FN = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
                            ctypes.c_uint64, ctypes.c_void_p)
 
@@ -107,6 +185,10 @@ EXPORTS = ("lso_adam_step", "lso_adam_step_noalloc", "lso_norm_workspace_bytes",
            "lso_stream_files", "lso_shadow_format", "lso_shadow_state", "lso_shadow_commit",
            "lso_stream_copy_mode", "lso_stream_stats", "lso_stream_slot_weight", "lso_stream_destroy", "lso_host_alloc",
            "lso_host_free", "lso_status_string", "lso_last_error")
+
+# every symbol include/lso_ops.h declares
+OPS_EXPORTS = ("lso_orthogonalize_workspace_bytes", "lso_orthogonalize", "lso_muon_workspace_bytes", "lso_muon_step",
+               "lso_embed_lookup", "lso_embed_grad_workspace_bytes", "lso_embed_grad", "lso_embed_producer")
 
 _lib = None
 _probes = None
@@ -166,6 +248,20 @@ def lib():
                      "lso_stream_layers", "lso_stream_files", "lso_shadow_format", "lso_shadow_state",
                      "lso_shadow_commit", "lso_stream_destroy", "lso_host_alloc", "lso_host_free"):
             getattr(L, name).restype = i32
+        for name in ("lso_orthogonalize", "lso_muon_step"):
+            getattr(L, name).argtypes = [vp, sz, vp, vp, u64, vp]
+            getattr(L, name).restype = i32
+        for name in ("lso_orthogonalize_workspace_bytes", "lso_muon_workspace_bytes"):
+            getattr(L, name).argtypes = [vp, sz, vp]
+            getattr(L, name).restype = u64
+        L.lso_embed_lookup.argtypes = [vp, vp]
+        L.lso_embed_lookup.restype = i32
+        L.lso_embed_grad_workspace_bytes.argtypes = [u64, u64, u64]
+        L.lso_embed_grad_workspace_bytes.restype = u64
+        L.lso_embed_grad.argtypes = [vp, vp, u64, vp]
+        L.lso_embed_grad.restype = i32
+        L.lso_embed_producer.argtypes = [vp, sz, vp, u64, vp]
+        L.lso_embed_producer.restype = i32
         _lib = L
     return _lib
 

@@ -1,6 +1,7 @@
 """Compile the HIP libraries in-tree for gfx950.
 
-liblso.so         the C ABI of include/lso.h (fused kernel, runtime, streams)
+liblso.so         the C ABI of include/lso.h (fused kernel, runtime, streams) and
+                  include/lso_ops.h (matrices, embedding)
 liblso_probes.so  measurement / verification probes (copy ceiling, BF16 cast)
 """
 from __future__ import annotations
@@ -29,7 +30,8 @@ LINK = ["-lhsa-runtime64"]
 
 LIBS = {
     "liblso.so": ["lso_adam.hip", "lso_copy.hip", "lso_tiled.hip", "lso_noalloc.hip", "lso_runtime.cpp",
-                  "lso_stream.cpp", "lso_io.cpp", "lso_shadow.cpp", "lso_sdma.cpp"],
+                  "lso_stream.cpp", "lso_io.cpp", "lso_shadow.cpp", "lso_sdma.cpp", "lso_matrix.cpp", "lso_ns.hip",
+                  "lso_embed.hip"],
     "liblso_probes.so": ["lso_probes.hip", "lso_probe_io.cpp", "lso_sdma.cpp"],
 }
 

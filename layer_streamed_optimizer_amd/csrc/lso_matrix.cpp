@@ -1,0 +1,342 @@
+// Host side of lso_orthogonalize and lso_muon_step: checks, the workspace
+// plan and the table of a call.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "lso_ns.h"
+#include "lso_ops.h"
+#include "lso_runtime.h"
+
+namespace lso {
+namespace {
+
+constexpr uint64_t kMaxSide = (1ull << 31) - 1;
+constexpr uint64_t kMaxIndex = (1ull << 24) - 8;   // workgroups of a launch: 256 lanes each, under 2^32 in all
+constexpr double kDefaultCoef[3] = {3.4445, -4.7750, 2.0315};
+
+// A matrix of either call, before its place in the plan.
+struct Item {
+    NsMat mat;
+    uint64_t rows, cols;
+};
+
+uint64_t padded(uint64_t n) { return (n + kNsTile - 1) / kNsTile * kNsTile; }
+
+int small_class(uint64_t k) { return k <= 8 ? 0 : k <= 16 ? 1 : k <= LSO_NS_SMALL_SIDE ? 2 : -1; }
+
+// The largest values that a run from s <= 1 can meet: of the iterates'
+// singular values s, of s^2 and of the polynomial a + b s^2 + c s^4; and for
+// each step the power of two that the polynomial stays under.
+double most_value(const double* coef, uint32_t steps, uint32_t* shift)
+{
+    double s = 1.0, most = 1.0;
+    for (uint32_t k = 0; k < steps; ++k) {
+        const double a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2], z = s * s;
+        double poly = std::max(std::fabs(a), std::fabs(a + b * z + c * z * z));
+        if (c != 0.0 && -b / (2 * c) > 0.0 && -b / (2 * c) < z) poly = std::max(poly, std::fabs(a - b * b / (4 * c)));
+        most = std::max({most, z, poly});
+        shift[k] = 0;
+        while (shift[k] < 4 && poly >= std::ldexp(1.0, static_cast<int>(shift[k]))) ++shift[k];
+        // s p(s^2) on [0, s]: at the end, and where 5 c t^2 + 3 b t + a = 0, t = s^2
+        auto value = [&](double t) { return std::sqrt(t) * std::fabs(a + t * (b + t * c)); };
+        double next = value(z);
+        const double disc = 9 * b * b - 20 * a * c;
+        if (c != 0.0 && disc >= 0.0) {
+            for (const double t : {(-3 * b + std::sqrt(disc)) / (10 * c), (-3 * b - std::sqrt(disc)) / (10 * c)})
+                if (t > 0.0 && t < z) next = std::max(next, value(t));
+        } else if (c == 0.0 && b != 0.0) {
+            const double t = -a / (3 * b);
+            if (t > 0.0 && t < z) next = std::max(next, value(t));
+        }
+        s = next;
+        most = std::max(most, s);
+    }
+    return most;
+}
+
+lso_status check_params(const lso_ns_params* p, NsCall& c)
+{
+    c.steps = p ? p->steps : 5;
+    c.eps = p ? p->eps : 1e-7;
+    if (p && p->precision > LSO_NS_HALF) return fail(LSO_E_INVALID, "unknown precision %u", p->precision);
+    if (c.steps < 1 || c.steps > LSO_NS_MAX_STEPS)
+        return fail(LSO_E_INVALID, "steps must be 1 to %u (got %u)", LSO_NS_MAX_STEPS, c.steps);
+    if (!(std::isfinite(c.eps) && c.eps >= 0.0)) return fail(LSO_E_INVALID, "eps must be finite and >= 0");
+    for (uint32_t k = 0; k < 3 * c.steps; ++k) {
+        c.coef[k] = p && p->coef ? p->coef[k] : kDefaultCoef[k % 3];
+        if (!std::isfinite(c.coef[k])) return fail(LSO_E_INVALID, "coefficient %u is not finite", k);
+    }
+    const double most = most_value(c.coef, c.steps, c.shift);
+    if (!(most <= kNsMostValue))
+        return fail(LSO_E_INVALID, "the coefficients let a value reach %.3g, more than %.3g", most, kNsMostValue);
+    return LSO_OK;
+}
+
+// Bytes from the first to the last element of rows x cols at stride ld.
+uint64_t span(uint64_t rows, uint64_t cols, uint64_t ld, uint64_t elem) { return ((rows - 1) * ld + cols) * elem; }
+
+lso_status check_sides(uint64_t rows, uint64_t cols, size_t i)
+{
+    if (rows > kMaxSide || cols > kMaxSide) return fail(LSO_E_INVALID, "matrix %zu: a side is too large", i);
+    if (rows != 0 && cols > (1ull << 56) / rows) return fail(LSO_E_INVALID, "matrix %zu: too many elements", i);
+    return LSO_OK;
+}
+
+lso_status take_array(std::vector<Interval>& iv, uintptr_t addr, uint64_t bytes, uint64_t elem, bool written, size_t i,
+                      const char* name)
+{
+    if (addr == 0) return fail(LSO_E_INVALID, "matrix %zu: %s address is NULL", i, name);
+    if (addr % elem != 0) return fail(LSO_E_ALIGN, "matrix %zu: %s is not aligned to its elements", i, name);
+    if (!add_array(iv, addr, bytes, written, i))
+        return fail(LSO_E_INVALID, "matrix %zu: %s range wraps the address space", i, name);
+    return LSO_OK;
+}
+
+// The checks of lso_orthogonalize; with iv, of its addresses too.
+lso_status collect(const lso_matrix* mats, size_t n, std::vector<Item>& items, std::vector<Interval>* iv, bool& all_bf16)
+{
+    if (n > 0 && !mats) return fail(LSO_E_INVALID, "mats is NULL");
+    all_bf16 = true;
+    for (size_t i = 0; i < n; ++i) {
+        const lso_matrix& a = mats[i];
+        for (const uint32_t d : {a.x_dtype, a.y_dtype})
+            if (d != LSO_DT_F32 && d != LSO_DT_BF16)
+                return fail(LSO_E_DTYPE, "matrix %zu: x and y must be F32 or BF16", i);
+        lso_status s = check_sides(a.rows, a.cols, i);
+        if (s != LSO_OK) return s;
+        if (a.rows == 0 || a.cols == 0) continue;
+        if (a.ld_x < a.cols || a.ld_y < a.cols || a.ld_x > kMaxSide || a.ld_y > kMaxSide)
+            return fail(LSO_E_INVALID, "matrix %zu: a row stride is smaller than cols, or too large", i);
+        if (a.y_dtype != LSO_DT_BF16) all_bf16 = false;
+        const uint64_t ex = a.x_dtype == LSO_DT_F32 ? 4 : 2, ey = a.y_dtype == LSO_DT_F32 ? 4 : 2;
+        if (iv) {
+            const bool same = a.x == a.y && a.x_dtype == a.y_dtype && a.ld_x == a.ld_y;
+            if (!same) {
+                s = take_array(*iv, reinterpret_cast<uintptr_t>(a.x), span(a.rows, a.cols, a.ld_x, ex), ex, false, i, "x");
+                if (s != LSO_OK) return s;
+            }
+            s = take_array(*iv, reinterpret_cast<uintptr_t>(a.y), span(a.rows, a.cols, a.ld_y, ey), ey, true, i, "y");
+            if (s != LSO_OK) return s;
+        }
+        Item it{};
+        it.rows = a.rows;
+        it.cols = a.cols;
+        it.mat.src = a.x;
+        it.mat.dst = a.y;
+        it.mat.ld_src = static_cast<uint32_t>(a.ld_x);
+        it.mat.ld_dst = static_cast<uint32_t>(a.ld_y);
+        it.mat.flags = (a.x_dtype == LSO_DT_F32 ? kNsSrcF32 : 0) | (a.y_dtype == LSO_DT_F32 ? kNsDstF32 : 0);
+        items.push_back(it);
+    }
+    return LSO_OK;
+}
+
+lso_status collect(const lso_muon_block* blocks, size_t n, std::vector<Item>& items, std::vector<Interval>* iv, bool& all_bf16)
+{
+    if (n > 0 && !blocks) return fail(LSO_E_INVALID, "blocks is NULL");
+    all_bf16 = false;   // the result is the FP32 master
+    for (size_t i = 0; i < n; ++i) {
+        const lso_muon_block& b = blocks[i];
+        if (b.grad_dtype != LSO_DT_BF16 && b.grad_dtype != LSO_DT_F32)
+            return fail(LSO_E_DTYPE, "matrix %zu: gradient dtype must be BF16 or F32", i);
+        if (b.weight_dtype != LSO_DT_BF16 && b.weight_dtype != LSO_DT_NONE)
+            return fail(LSO_E_DTYPE, "matrix %zu: weight dtype must be BF16 or NONE", i);
+        if ((b.flags & ~LSO_MUON_NESTEROV) != 0 || b.reserved != 0)
+            return fail(LSO_E_INVALID, "matrix %zu: unknown flags or reserved field", i);
+        if (!std::isfinite(b.lr) || !std::isfinite(b.weight_decay) || !std::isfinite(b.scale))
+            return fail(LSO_E_INVALID, "matrix %zu: lr, weight_decay and scale must be finite", i);
+        if (!(b.beta >= 0.0 && b.beta < 1.0)) return fail(LSO_E_INVALID, "matrix %zu: beta must be in [0, 1)", i);
+        lso_status s = check_sides(b.rows, b.cols, i);
+        if (s != LSO_OK) return s;
+        if (b.rows == 0 || b.cols == 0) continue;
+        const uintptr_t base = reinterpret_cast<uintptr_t>(b.base);
+        const uint64_t count = b.rows * b.cols, eg = b.grad_dtype == LSO_DT_F32 ? 4 : 2;
+        const bool weight = b.weight_dtype == LSO_DT_BF16;
+        if (iv) {
+            const struct { uint64_t off, elem; bool used, written; const char* name; } arr[4] = {
+                {b.off_master, 4, true, true, "master"},
+                {b.off_m, 4, true, true, "m"},
+                {b.off_grad, eg, true, false, "grad"},
+                {b.off_weight, 2, weight, true, "weight"},
+            };
+            for (const auto& a : arr) {
+                if (!a.used) continue;
+                s = take_array(*iv, base + a.off, count * a.elem, a.elem, a.written, i, a.name);
+                if (s != LSO_OK) return s;
+            }
+        }
+        Item it{};
+        it.rows = b.rows;
+        it.cols = b.cols;
+        it.mat.src = reinterpret_cast<const void*>(base + b.off_grad);
+        it.mat.dst = weight ? reinterpret_cast<void*>(base + b.off_weight) : nullptr;
+        it.mat.m = reinterpret_cast<float*>(base + b.off_m);
+        it.mat.master = reinterpret_cast<float*>(base + b.off_master);
+        it.mat.ld_src = it.mat.ld_dst = static_cast<uint32_t>(b.cols);
+        it.mat.flags = kNsMuon | (eg == 4 ? kNsSrcF32 : 0) | ((b.flags & LSO_MUON_NESTEROV) ? kNsNesterov : 0);
+        it.mat.beta = static_cast<float>(b.beta);
+        it.mat.c1 = static_cast<float>(1.0 - b.beta);
+        it.mat.keep = static_cast<float>(1.0 - b.lr * b.weight_decay);
+        it.mat.step = static_cast<float>(-b.lr * b.scale);
+        if (!std::isfinite(it.mat.keep) || !std::isfinite(it.mat.step))
+            return fail(LSO_E_INVALID, "matrix %zu: lr * weight_decay or lr * scale is not an FP32 number", i);
+        items.push_back(it);
+    }
+    return LSO_OK;
+}
+
+// Order the items (small path by class, then the general path), give each
+// its part of the workspace and its first index in every launch.  work is
+// the workspace's address (0 to plan only); returns the bytes needed, the
+// table's first, or 0 with an error set.
+uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<NsMat>& table)
+{
+    uint64_t at = (items.size() * sizeof(NsMat) + 255) / 256 * 256;
+    table.clear();
+    table.reserve(items.size());
+    for (int cls = 0; cls <= kNsClasses; ++cls) {
+        uint64_t chunks = 0, prep = 0, sym = 0, apply = 0;
+        uint32_t count = 0;
+        for (const Item& it : items) {
+            const uint64_t k = std::min(it.rows, it.cols), l = std::max(it.rows, it.cols);
+            const int own = small_class(k);
+            if ((own < 0 ? kNsClasses : own) != cls) continue;
+            NsMat m = it.mat;
+            m.rows = static_cast<uint32_t>(it.rows);
+            m.cols = static_cast<uint32_t>(it.cols);
+            if (it.rows > it.cols) m.flags |= kNsTall;
+            m.work = reinterpret_cast<char*>(work + at);
+            if (own >= 0) {
+                m.prep0 = static_cast<uint32_t>(chunks);
+                chunks += (l + kNsSmallChunk - 1) / kNsSmallChunk;
+                at += ns_small_bytes(k, l);
+            } else {
+                const uint64_t mp = padded(k), np = padded(l), tm = mp / kNsTile, tn = np / kNsTile;
+                if (mp > (1u << 20) || np > kMaxSide) {
+                    fail(LSO_E_INVALID, "a matrix of %llu x %llu is too large", static_cast<unsigned long long>(it.rows),
+                         static_cast<unsigned long long>(it.cols));
+                    return 0;
+                }
+                m.mp = static_cast<uint32_t>(mp);
+                m.np = static_cast<uint32_t>(np);
+                m.prep0 = static_cast<uint32_t>(prep);
+                m.sym0 = static_cast<uint32_t>(sym);
+                m.apply0 = static_cast<uint32_t>(apply);
+                prep += mp / kNsPrep * (np / kNsPrep);
+                sym += tm * (tm + 1) / 2;
+                apply += tm * tn;
+                at += ns_work(mp, np, c.gram_terms).bytes;
+            }
+            ++count;
+            if (std::max({chunks, prep, sym, apply, uint64_t{count} * 4}) > kMaxIndex) {
+                fail(LSO_E_INVALID, "the call is too large: split it");
+                return 0;
+            }
+            table.push_back(m);
+        }
+        if (cls < kNsClasses) {
+            c.nsmall[cls] = count;
+            c.small_chunks[cls] = static_cast<uint32_t>(chunks);
+        } else {
+            c.nbig = count;
+            c.prep_tiles = static_cast<uint32_t>(prep);
+            c.sym_tiles = static_cast<uint32_t>(sym);
+            c.apply_tiles = static_cast<uint32_t>(apply);
+        }
+    }
+    return at;
+}
+
+uint32_t gram_terms(const lso_ns_params* p, bool all_bf16)
+{
+    const uint32_t precision = p ? p->precision : LSO_NS_AUTO;
+    if (precision == LSO_NS_AUTO) return all_bf16 ? 1 : 2;
+    return precision == LSO_NS_HALF ? 1 : 2;
+}
+
+template <typename T>
+uint64_t workspace_bytes(const T* list, size_t n, const lso_ns_params* params)
+{
+    clear_error();
+    NsCall c{};
+    std::vector<Item> items;
+    std::vector<NsMat> table;
+    bool all_bf16;
+    if (check_params(params, c) != LSO_OK || collect(list, n, items, nullptr, all_bf16) != LSO_OK) return 0;
+    c.gram_terms = gram_terms(params, all_bf16);
+    return plan(items, c, 0, table);
+}
+
+template <typename T>
+lso_status run(const T* list, size_t n, const lso_ns_params* params, void* workspace, uint64_t bytes, void* stream)
+{
+    clear_error();
+    NsCall c{};
+    std::vector<Item> items;
+    std::vector<NsMat> table;
+    std::vector<Interval> iv;
+    bool all_bf16;
+    lso_status s = check_params(params, c);
+    if (s == LSO_OK) s = collect(list, n, items, &iv, all_bf16);
+    if (s != LSO_OK) return s;
+    if (items.empty()) return LSO_OK;
+    c.gram_terms = gram_terms(params, all_bf16);
+    if (!workspace) return fail(LSO_E_INVALID, "workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return fail(LSO_E_ALIGN, "workspace must be 16-byte aligned");
+    const uint64_t need = plan(items, c, reinterpret_cast<uintptr_t>(workspace), table);
+    if (need == 0) return LSO_E_INVALID;
+    if (bytes < need)
+        return fail(LSO_E_INVALID, "workspace of %llu bytes is smaller than the %llu this call needs",
+                    static_cast<unsigned long long>(bytes), static_cast<unsigned long long>(need));
+    if (!add_array(iv, reinterpret_cast<uintptr_t>(workspace), need, true, n))
+        return fail(LSO_E_INVALID, "workspace range wraps the address space");
+    s = check_overlap(iv);
+    if (s != LSO_OK) return s;
+    c.table = table.data();
+    const int err = ns_launch(c, static_cast<NsMat*>(workspace), stream);
+    return err == 0 ? LSO_OK : hip_fail(err, "Newton-Schulz launch");
+}
+
+// std::bad_alloc does not cross the ABI.
+template <typename F, typename R>
+R guarded(F f, R none)
+{
+    try {
+        return f();
+    } catch (const std::exception& e) {
+        fail(LSO_E_NOMEM, "host memory: %s", e.what());
+        return none;
+    }
+}
+
+}  // namespace
+}  // namespace lso
+
+extern "C" {
+
+uint64_t lso_orthogonalize_workspace_bytes(const lso_matrix* mats, size_t n, const lso_ns_params* params)
+{
+    return lso::guarded([&] { return lso::workspace_bytes(mats, n, params); }, uint64_t{0});
+}
+
+lso_status lso_orthogonalize(const lso_matrix* mats, size_t n, const lso_ns_params* params, void* workspace,
+                             uint64_t workspace_bytes, void* stream)
+{
+    return lso::guarded([&] { return lso::run(mats, n, params, workspace, workspace_bytes, stream); }, LSO_E_NOMEM);
+}
+
+uint64_t lso_muon_workspace_bytes(const lso_muon_block* blocks, size_t n, const lso_ns_params* params)
+{
+    return lso::guarded([&] { return lso::workspace_bytes(blocks, n, params); }, uint64_t{0});
+}
+
+lso_status lso_muon_step(const lso_muon_block* blocks, size_t n, const lso_ns_params* params, void* workspace,
+                         uint64_t workspace_bytes, void* stream)
+{
+    return lso::guarded([&] { return lso::run(blocks, n, params, workspace, workspace_bytes, stream); }, LSO_E_NOMEM);
+}
+
+}  // extern "C"

@@ -1,0 +1,107 @@
+// Internal types of the Newton-Schulz path, shared by its host side
+// (lso_matrix.cpp) and its kernels (lso_ns.hip).
+#pragma once
+
+#include <cstdint>
+
+namespace lso {
+
+// Operands are FP16 numbers of the values times kNsScale (a power of two, so
+// scaling is exact): a matrix of Frobenius norm 1 and some million elements
+// has elements of about 2^-12, which the scale brings to the middle of
+// FP16's range, and no element of an iterate (at most kNsMostValue) passes
+// its end.
+constexpr float kNsScale = 4096.0f;
+constexpr double kNsMostValue = 15.9;
+
+// Edge of a product tile; the sides of a workspace matrix are multiples of it.
+constexpr uint32_t kNsTile = 128;
+// Edge of the square tiles of the elementwise passes.
+constexpr uint32_t kNsPrep = 64;
+// Elements along the long side per workgroup of the small path.
+constexpr uint32_t kNsSmallChunk = 256;
+// The small path's kernels are built for smaller sides up to 8, 16 and 32.
+constexpr int kNsClasses = 3;
+constexpr uint32_t kNsMaxSteps = 16;
+
+enum : uint32_t {
+    kNsSrcF32 = 1u,     // x or gradient is FP32 (else BF16)
+    kNsDstF32 = 2u,     // y is FP32 (else BF16)
+    kNsTall = 4u,       // rows > cols: the transpose is iterated on
+    kNsMuon = 8u,       // update: src is the gradient, dst the weight (or null)
+    kNsNesterov = 16u,
+};
+
+// One matrix of a call (an entry of the table in the workspace).
+struct NsMat {
+    const void* src;    // x, or the gradient
+    void* dst;          // y, or the BF16 weight or null
+    float* m;           // update only
+    float* master;      // update only
+    char* work;         // its part of the workspace
+    uint32_t rows, cols;
+    uint32_t ld_src, ld_dst;
+    uint32_t flags;
+    float beta, c1;     // beta, 1 - beta
+    float keep, step;   // 1 - lr weight_decay, -lr scale
+    uint32_t mp, np;    // padded smaller and larger side (general path)
+    // first index of this matrix in the index space of each launch
+    uint32_t prep0;     // kNsPrep tiles of the padded matrix; small path: chunks
+    uint32_t sym0;      // tiles on and under the diagonal of S
+    uint32_t apply0;    // tiles of X
+    uint32_t pad[2];
+};
+static_assert(sizeof(NsMat) == 104, "NsMat layout");
+
+// Offsets of a general-path matrix inside its part of the workspace:
+// X (smaller side by larger, gram_terms FP16 numbers per value, read by the
+// product S = X X^T), its transpose twice (two numbers per value, read and
+// written in turn by the product with the polynomial P), S and P.
+struct NsWork {
+    uint64_t x, xt[2], s, p, partial, inv, bytes;
+};
+#if defined(__HIPCC__)
+__host__ __device__
+#endif
+inline NsWork ns_work(uint64_t mp, uint64_t np, uint64_t gram_terms)
+{
+    const uint64_t xs = mp * np * 2, ss = mp * mp * 2 * gram_terms;   // multiples of 256
+    NsWork w{};
+    w.x = 0;
+    w.xt[0] = xs * gram_terms;
+    w.xt[1] = w.xt[0] + 2 * xs;
+    w.s = w.xt[1] + 2 * xs;
+    w.p = w.s + ss;
+    w.inv = w.p + ss;
+    w.partial = w.inv + 256;
+    w.bytes = w.partial + (mp / kNsPrep * (np / kNsPrep) * 8 + 255) / 256 * 256;
+    return w;
+}
+
+// Of a small-path matrix: the FP64 partial products of each chunk, and the
+// k x k matrix that x is multiplied by.
+inline uint64_t ns_small_bytes(uint64_t k, uint64_t l)
+{
+    const uint64_t chunks = (l + kNsSmallChunk - 1) / kNsSmallChunk;
+    return ((chunks + 1) * k * k * 8 + 255) / 256 * 256;
+}
+
+// One call, as the launches need it.  The table holds the small-path
+// matrices by class, then the others.
+struct NsCall {
+    const NsMat* table;                    // host copy
+    uint32_t nsmall[kNsClasses], nbig;
+    uint32_t small_chunks[kNsClasses];     // index spaces
+    uint32_t prep_tiles, sym_tiles, apply_tiles;
+    uint32_t gram_terms;                   // 1 or 2
+    uint32_t steps;
+    double eps;
+    double coef[3 * kNsMaxSteps];
+    uint32_t shift[kNsMaxSteps];           // a step multiplies X by less than 2^shift
+};
+
+// Enqueue the table's upload to device_table and every launch (lso_ns.hip).
+// Returns the hipError_t.
+int ns_launch(const NsCall& c, NsMat* device_table, void* stream);
+
+}  // namespace lso

@@ -69,14 +69,6 @@ uint64_t tiled_bytes(uint64_t n)
     return 12ull * LSO_TILE_ELEMS * ((n + LSO_TILE_ELEMS - 1) / LSO_TILE_ELEMS);
 }
 
-namespace {
-
-struct Interval {
-    uintptr_t lo, hi;   // [lo, hi)
-    bool written;
-    size_t block;
-};
-
 lso_status check_overlap(std::vector<Interval>& iv)
 {
     std::sort(iv.begin(), iv.end(), [](const Interval& a, const Interval& b) { return a.lo < b.lo; });
@@ -101,8 +93,6 @@ bool add_array(std::vector<Interval>& iv, uintptr_t addr, uint64_t bytes, bool w
     iv.push_back({addr, addr + bytes, written, block});
     return true;
 }
-
-}  // namespace
 
 namespace {
 

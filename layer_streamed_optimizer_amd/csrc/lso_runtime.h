@@ -3,6 +3,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <vector>
 
 #include "lso.h"
 
@@ -15,6 +16,16 @@ void clear_error();
 
 // Count one fused-update kernel launch (lso_kernel_launches).
 void count_launch();
+
+// An array of a call, and the check that no written one overlaps another
+// (sorts iv).  add_array returns false if the range wraps the address space.
+struct Interval {
+    uintptr_t lo, hi;   // [lo, hi)
+    bool written;
+    size_t block;
+};
+lso_status check_overlap(std::vector<Interval>& iv);
+bool add_array(std::vector<Interval>& iv, uintptr_t addr, uint64_t bytes, bool written, size_t block);
 
 // Bytes of the tiled state region of n parameters.
 uint64_t tiled_bytes(uint64_t n);
