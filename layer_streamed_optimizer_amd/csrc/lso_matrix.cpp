@@ -23,7 +23,7 @@ struct Item {
     uint64_t rows, cols;
 };
 
-uint64_t padded(uint64_t n) { return (n + kNsTile - 1) / kNsTile * kNsTile; }
+uint64_t padded(uint64_t n, uint64_t tile) { return (n + tile - 1) / tile * tile; }
 
 int small_class(uint64_t k) { return k <= 8 ? 0 : k <= 16 ? 1 : k <= LSO_NS_SMALL_SIDE ? 2 : -1; }
 
@@ -188,17 +188,71 @@ lso_status collect(const lso_muon_block* blocks, size_t n, std::vector<Item>& it
     return LSO_OK;
 }
 
-// Order the items (small path by class, then the general path), give each
-// its part of the workspace and its first index in every launch.  work is
-// the workspace's address (0 to plan only); returns the bytes needed, the
-// table's first, or 0 with an error set.
+// How the products of the general path are cut up.  A launch should give
+// each of the GPU's 256 CUs the same work: `slots` workgroups run at a time,
+// so the tiles' summed index is cut into parts of `depth` stages such that
+// the parts fill a whole number of rounds of slots; the cost of a round is its
+// depth plus kPartCost stages (filling the pipeline, storing and adding up
+// the sums).
+struct Tiles {
+    uint64_t count, stages;   // of one matrix in one launch
+};
+constexpr uint64_t kPartCost = 16;
+
+uint64_t units_of(const std::vector<Tiles>& list, uint64_t depth)
+{
+    uint64_t units = 0;
+    for (const Tiles& t : list) units += (t.count * ((t.stages + depth - 1) / depth) + 7) / 8 * 8;
+    return units;
+}
+
+uint32_t part_depth(const std::vector<Tiles>& list, uint64_t slots)
+{
+    uint64_t most = 1;
+    for (const Tiles& t : list) most = std::max(most, t.stages);
+    const uint64_t whole_units = units_of(list, most);
+    if (whole_units > 8 * slots) return static_cast<uint32_t>(most);   // many rounds: nothing to gain
+    uint64_t best = most, best_cost = (whole_units + slots - 1) / slots * (most + kPartCost / 2);
+    for (uint64_t depth = most - 1; depth >= 8; --depth) {
+        const uint64_t units = units_of(list, depth), cost = (units + slots - 1) / slots * (depth + kPartCost);
+        if (cost < best_cost) {
+            best = depth;
+            best_cost = cost;
+        }
+        if (units > 8 * slots) break;
+    }
+    return static_cast<uint32_t>(best);
+}
+
+uint32_t tile_edge(const std::vector<Item>& items)
+{
+    uint64_t tiles = 0;
+    for (const Item& it : items) {
+        const uint64_t k = std::min(it.rows, it.cols), l = std::max(it.rows, it.cols);
+        if (small_class(k) < 0) tiles += padded(k, 256) / 256 * (padded(l, 256) / 256);
+    }
+    return tiles >= 512 ? 256 : 128;
+}
+
+// Order the items (small path by class, then the general path, deep matrices
+// first), give each its part of the workspace and its first index in every
+// launch.  work is the workspace's address (0 to plan only); returns the
+// bytes needed, the table's first, or 0 with an error set.
 uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<NsMat>& table)
 {
     uint64_t at = (items.size() * sizeof(NsMat) + 255) / 256 * 256;
     table.clear();
     table.reserve(items.size());
+    // a launch ends sooner if the longest units start first
+    std::stable_sort(items.begin(), items.end(), [](const Item& a, const Item& b) {
+        return std::max(a.rows, a.cols) > std::max(b.rows, b.cols);
+    });
+    c.tile = tile_edge(items);
+    const uint64_t edge = c.tile;
+    std::vector<Tiles> lists[3];
+    uint64_t most_index = 0;
     for (int cls = 0; cls <= kNsClasses; ++cls) {
-        uint64_t chunks = 0, prep = 0, sym = 0, apply = 0;
+        uint64_t chunks = 0, prep = 0;
         uint32_t count = 0;
         for (const Item& it : items) {
             const uint64_t k = std::min(it.rows, it.cols), l = std::max(it.rows, it.cols);
@@ -214,8 +268,8 @@ uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<N
                 chunks += (l + kNsSmallChunk - 1) / kNsSmallChunk;
                 at += ns_small_bytes(k, l);
             } else {
-                const uint64_t mp = padded(k), np = padded(l), tm = mp / kNsTile, tn = np / kNsTile;
-                if (mp > (1u << 20) || np > kMaxSide) {
+                const uint64_t mp = padded(k, edge), np = padded(l, edge), tm = mp / edge, tn = np / edge;
+                if (mp > (1u << 20) || np > kMaxSide / 4) {
                     fail(LSO_E_INVALID, "a matrix of %llu x %llu is too large", static_cast<unsigned long long>(it.rows),
                          static_cast<unsigned long long>(it.cols));
                     return 0;
@@ -223,18 +277,15 @@ uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<N
                 m.mp = static_cast<uint32_t>(mp);
                 m.np = static_cast<uint32_t>(np);
                 m.prep0 = static_cast<uint32_t>(prep);
-                m.sym0 = static_cast<uint32_t>(sym);
-                m.apply0 = static_cast<uint32_t>(apply);
                 prep += mp / kNsPrep * (np / kNsPrep);
-                sym += tm * (tm + 1) / 2;
-                apply += tm * tn;
                 at += ns_work(mp, np, c.gram_terms).bytes;
+                const uint64_t values = c.gram_terms == 1 ? 32 : 16;   // of the summed index per stage
+                lists[0].push_back({tm * (tm + 1) / 2, np / values});
+                lists[1].push_back({tm * (tm + 1) / 2, mp / values});
+                lists[2].push_back({tm * tn, mp / 16});
             }
             ++count;
-            if (std::max({chunks, prep, sym, apply, uint64_t{count} * 4}) > kMaxIndex) {
-                fail(LSO_E_INVALID, "the call is too large: split it");
-                return 0;
-            }
+            most_index = std::max({most_index, chunks, prep, uint64_t{count} * 4});
             table.push_back(m);
         }
         if (cls < kNsClasses) {
@@ -243,9 +294,42 @@ uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<N
         } else {
             c.nbig = count;
             c.prep_tiles = static_cast<uint32_t>(prep);
-            c.sym_tiles = static_cast<uint32_t>(sym);
-            c.apply_tiles = static_cast<uint32_t>(apply);
         }
+    }
+    if (c.nbig > 0) {
+        NsProduct* products[3] = {&c.gram, &c.poly, &c.apply};
+        uint32_t NsMat::*firsts[3] = {&NsMat::gram0, &NsMat::poly0, &NsMat::apply0};
+        uint64_t most_units = 0, part_units = 0;
+        for (int p = 0; p < 3; ++p) {
+            const uint64_t units_before = units_of(lists[p], UINT32_MAX);
+            if (units_before > kMaxIndex) {
+                most_index = units_before;
+                break;
+            }
+            products[p]->depth = part_depth(lists[p], edge == 256 ? 256 : 512);
+            uint64_t units = 0;
+            bool cut = false;
+            NsMat* m = table.data() + (table.size() - c.nbig);
+            for (const Tiles& t : lists[p]) {
+                const uint64_t parts = (t.stages + products[p]->depth - 1) / products[p]->depth;
+                (m++)->*firsts[p] = static_cast<uint32_t>(units);
+                units += (t.count * parts + 7) / 8 * 8;
+                cut = cut || parts > 1;
+            }
+            products[p]->units = static_cast<uint32_t>(units);
+            most_units = std::max(most_units, units);
+            if (cut) part_units = std::max(part_units, units);
+        }
+        most_index = std::max(most_index, most_units);
+        c.counters = reinterpret_cast<uint32_t*>(work + at);
+        c.ncounters = static_cast<uint32_t>(part_units);
+        at += (part_units * 4 + 255) / 256 * 256;
+        c.parts = reinterpret_cast<float*>(work + at);
+        at += part_units * edge * edge * 4;
+    }
+    if (most_index > kMaxIndex) {
+        fail(LSO_E_INVALID, "the call is too large: split it");
+        return 0;
     }
     return at;
 }

@@ -14,8 +14,6 @@ namespace lso {
 constexpr float kNsScale = 4096.0f;
 constexpr double kNsMostValue = 15.9;
 
-// Edge of a product tile; the sides of a workspace matrix are multiples of it.
-constexpr uint32_t kNsTile = 128;
 // Edge of the square tiles of the elementwise passes.
 constexpr uint32_t kNsPrep = 64;
 // Elements along the long side per workgroup of the small path.
@@ -47,9 +45,10 @@ struct NsMat {
     uint32_t mp, np;    // padded smaller and larger side (general path)
     // first index of this matrix in the index space of each launch
     uint32_t prep0;     // kNsPrep tiles of the padded matrix; small path: chunks
-    uint32_t sym0;      // tiles on and under the diagonal of S
-    uint32_t apply0;    // tiles of X
-    uint32_t pad[2];
+    uint32_t gram0;     // units (tile, part of the summed index) of S, a multiple of 8 per matrix
+    uint32_t poly0;     // of the polynomial
+    uint32_t apply0;    // of X
+    uint32_t pad;
 };
 static_assert(sizeof(NsMat) == 104, "NsMat layout");
 
@@ -86,13 +85,23 @@ inline uint64_t ns_small_bytes(uint64_t k, uint64_t l)
     return ((chunks + 1) * k * k * 8 + 255) / 256 * 256;
 }
 
+// A product's launch: workgroups, and stages of the summed index per part.
+struct NsProduct {
+    uint32_t units, depth;
+};
+
 // One call, as the launches need it.  The table holds the small-path
 // matrices by class, then the others.
 struct NsCall {
     const NsMat* table;                    // host copy
     uint32_t nsmall[kNsClasses], nbig;
     uint32_t small_chunks[kNsClasses];     // index spaces
-    uint32_t prep_tiles, sym_tiles, apply_tiles;
+    uint32_t prep_tiles;
+    NsProduct gram, poly, apply;
+    uint32_t tile;                         // edge of a product tile: 128 or 256
+    float* parts;                          // workspace of the parts' sums
+    uint32_t* counters;
+    uint32_t ncounters;
     uint32_t gram_terms;                   // 1 or 2
     uint32_t steps;
     double eps;

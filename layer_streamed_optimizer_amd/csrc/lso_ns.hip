@@ -12,10 +12,11 @@
 // Operands.  A value v is held as h + l, h = fp16(v * 4096), l =
 // fp16(v * 4096 - h): 22 significant bits.  A product of two such matrices
 // is three matrix-core products, h h + h l + l h, summed in the same FP32
-// registers (l l is below FP32's rounding); with one term it is one.  All
-// operands are stored with the summed index contiguous, so X and X^T are
-// both kept; h and l of 32 consecutive values sit next to each other (64 B
-// each), so a row of a product's stage is always one 128-byte line.
+// registers (l l is below FP32's rounding); with one term it is one.  The
+// summed index of every operand runs along its rows, so X and X^T are both
+// kept.  An operand is stored in blocks of kT rows (the edge of a product's
+// tile) by 16 values, 32 bytes a row and term, one after another along the
+// rows: what a product loads at a time is one run of memory.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -27,6 +28,7 @@ namespace lso {
 namespace {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -139,8 +141,11 @@ __device__ __forceinline__ void prep_tile(const NsMat& m, uint32_t t, uint32_t& 
     c0 = t % across * kNsPrep;
 }
 
-__global__ void __launch_bounds__(256) ns_norm_kernel(const NsMat* tab, uint32_t n, uint32_t gram_terms)
+__global__ void __launch_bounds__(256) ns_norm_kernel(const NsMat* tab, uint32_t n, uint32_t gram_terms, uint32_t* counters,
+                                                      uint32_t ncounters)
 {
+    // the products' counters start at zero
+    for (uint32_t k = blockIdx.x * 256 + threadIdx.x; k < ncounters; k += gridDim.x * 256) counters[k] = 0;
     const uint32_t i = find_mat<&NsMat::prep0>(tab, n, blockIdx.x);
     const NsMat m = load_mat(tab, i);
     uint32_t r0, c0;
@@ -196,10 +201,27 @@ __global__ void __launch_bounds__(1024) ns_scale_kernel(const NsMat* tab, uint32
     *reinterpret_cast<NsScaling*>(m.work + w.inv) = s;
 }
 
-// Eight consecutive values v (already scaled) as FP16 terms into row `row`
-// (of `ld` values) from column c (a multiple of 8) of an operand.
+// Where the 16 bytes of term `term` of values (row, c .. c + 7) of an operand
+// are (c a multiple of 8, ld its padded row length).  The pieces of a row in
+// a block are permuted by the row's number, so that the sixteen lanes which
+// read LDS together (64 banks) hit all banks once a block has been copied
+// there as it is.
 template <int kTerms>
-__device__ __forceinline__ void put_terms(char* base, uint64_t row, uint64_t ld, uint32_t c, const float (&v)[8])
+__device__ __forceinline__ uint32_t swizzle(uint32_t row)
+{
+    return kTerms == 2 ? ((row >> 2) & 3u) : ((row >> 3) & 1u);
+}
+
+template <int kT, int kTerms>
+__device__ __forceinline__ uint64_t piece_at(uint32_t row, uint32_t ld, uint32_t c, uint32_t term)
+{
+    const uint32_t r = row % kT, piece = (term * 2 + (c % 16) / 8) ^ swizzle<kTerms>(r);
+    return (static_cast<uint64_t>(row / kT) * (ld / 16) + c / 16) * (kT * 32 * kTerms) + r * (32 * kTerms) + piece * 16;
+}
+
+// Eight consecutive values v (already scaled) as FP16 terms.
+template <int kT, int kTerms>
+__device__ __forceinline__ void put_terms(char* base, uint32_t row, uint32_t ld, uint32_t c, const float (&v)[8])
 {
     f16x8 h, l;
 #pragma unroll
@@ -207,28 +229,32 @@ __device__ __forceinline__ void put_terms(char* base, uint64_t row, uint64_t ld,
         h[e] = static_cast<_Float16>(v[e]);
         l[e] = static_cast<_Float16>(v[e] - static_cast<float>(h[e]));
     }
-    if (kTerms == 1) {
-        *reinterpret_cast<f16x8*>(base + (row * ld + c) * 2) = h;
-    } else {
-        char* p = base + (row * ld + (c & ~31u)) * 4 + (c & 31u) * 2;
-        *reinterpret_cast<f16x8*>(p) = h;
-        *reinterpret_cast<f16x8*>(p + 64) = l;
+    *reinterpret_cast<f16x8*>(base + piece_at<kT, kTerms>(row, ld, c, 0)) = h;
+    if (kTerms == 2) *reinterpret_cast<f16x8*>(base + piece_at<kT, kTerms>(row, ld, c, 1)) = l;
+}
+
+// Eight consecutive values, times kNsScale.
+template <int kT, int kTerms>
+__device__ __forceinline__ void get_terms(const char* base, uint32_t row, uint32_t ld, uint32_t c, float (&v)[8])
+{
+    const f16x8 h = *reinterpret_cast<const f16x8*>(base + piece_at<kT, kTerms>(row, ld, c, 0));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(h[e]);
+    if (kTerms == 2) {
+        const f16x8 l = *reinterpret_cast<const f16x8*>(base + piece_at<kT, kTerms>(row, ld, c, 1));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += static_cast<float>(l[e]);
     }
 }
 
-__device__ __forceinline__ void put_terms_n(uint32_t terms, char* base, uint64_t row, uint64_t ld, uint32_t c, const float (&v)[8])
-{
-    if (terms == 1) put_terms<1>(base, row, ld, c, v);
-    else put_terms<2>(base, row, ld, c, v);
-}
-
 // X_0 and its transpose from u, zeros in the padding.
-__global__ void __launch_bounds__(256) ns_split_kernel(const NsMat* tab, uint32_t n, uint32_t gram_terms)
+template <int kT, int kGramTerms>
+__global__ void __launch_bounds__(256) ns_split_kernel(const NsMat* tab, uint32_t n)
 {
     __shared__ float tile[kNsPrep][kNsPrep + 1];
     const uint32_t i = find_mat<&NsMat::prep0>(tab, n, blockIdx.x);
     const NsMat m = load_mat(tab, i);
-    const NsWork w = ns_work(m.mp, m.np, gram_terms);
+    const NsWork w = ns_work(m.mp, m.np, kGramTerms);
     uint32_t r0, c0;
     prep_tile(m, blockIdx.x - m.prep0, r0, c0);
     const double inv = reinterpret_cast<const NsScaling*>(m.work + w.inv)->inv;
@@ -244,9 +270,9 @@ __global__ void __launch_bounds__(256) ns_split_kernel(const NsMat* tab, uint32_
     const bool tall = (m.flags & kNsTall) != 0;
     char* xt = m.work + w.xt[0];
     char* x = m.work + w.x;
-    // natural orientation: rows x cols is X, or X^T if tall
+    // natural orientation: rows x cols is X, or X^T if tall; two lanes per row of a block
     for (uint32_t v = threadIdx.x; v < kNsPrep * kNsPrep / 8; v += 256) {
-        const uint32_t r = v >> 3, c = (v & 7u) * 8;
+        const uint32_t c = (v & 1u) * 8 + v / (kNsPrep * 2) * 16, r = (v >> 1) % kNsPrep;
         float a[8], b[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -254,175 +280,385 @@ __global__ void __launch_bounds__(256) ns_split_kernel(const NsMat* tab, uint32_
             b[e] = tile[c + e][r];
         }
         if (tall) {
-            put_terms<2>(xt, r0 + r, m.mp, c0 + c, a);
-            put_terms_n(gram_terms, x, c0 + r, m.np, r0 + c, b);
+            put_terms<kT, 2>(xt, r0 + r, m.mp, c0 + c, a);
+            put_terms<kT, kGramTerms>(x, c0 + r, m.np, r0 + c, b);
         } else {
-            put_terms_n(gram_terms, x, r0 + r, m.np, c0 + c, a);
-            put_terms<2>(xt, c0 + r, m.mp, r0 + c, b);
+            put_terms<kT, kGramTerms>(x, r0 + r, m.np, c0 + c, a);
+            put_terms<kT, 2>(xt, c0 + r, m.mp, r0 + c, b);
         }
     }
 }
 
 // ------------------------------------------------------ general path: products
 //
-// D[i][j] = sum over k of A[i][k] B[j][k], a 128 x 128 tile per workgroup of
-// four waves, 64 x 64 each (2 x 2 matrix-core tiles of 32 x 32).  A stage is
-// 128 bytes of each row of a two-term operand (32 values, h and l) or of a
-// one-term operand multiplied by one (64 values), 64 bytes of a one-term
-// operand multiplied by a two-term one; two stages alternate in LDS, the
-// next one loaded straight to LDS while the current one is multiplied.
-// 16-byte pieces of a row are permuted by the row's number so that the eight
-// lanes which read LDS together hit all banks; the permutation is made by
-// the global address each lane loads from, since a load to LDS writes
-// consecutive lanes to consecutive places.
+// D[i][j] = sum over k of A[i][k] B[j][k], one tile of kT x kT per workgroup.
+// kT = 128: four waves, 64 x 64 each; kT = 256: eight waves, 128 x 64 each;
+// in matrix-core tiles of 32 x 32.  A stage is one block of each operand (two
+// where both have one term); stages go round four buffers in LDS, loaded
+// straight to LDS three stages ahead of the one that is multiplied.
+//
+// Where a launch has too few tiles for the 256 CUs, the summed index of a tile
+// is cut into parts, one workgroup each.  Each leaves its FP32 sums in the
+// workspace and the last one to finish (a counter per tile) adds them up in
+// the order of the parts, so the result does not depend on which that is.
+// Nobody waits for another workgroup.
 
-constexpr uint32_t kPitch = kNsTile + 1;   // of the result tile in LDS
-
-template <int kRowBytes>
-__device__ __forceinline__ uint32_t swizzle(uint32_t row)
+// Copy kBytes from g to lds, by all waves.
+template <int kWaves, uint32_t kBytes>
+__device__ __forceinline__ void load_stage(const char* g, char* lds, uint32_t wave, uint32_t lane)
 {
-    return kRowBytes == 128 ? (row & 7u) : ((row >> 1) & 3u);
-}
-
-// Load stage rows [0, 128) x kRowBytes from g (row stride bytes) to lds.
-template <int kRowBytes>
-__device__ __forceinline__ void load_stage(const char* g, uint32_t stride, char* lds)
-{
-    constexpr uint32_t kPieces = kRowBytes / 16, kRowsPerLoad = 64 / kPieces, kLoads = kNsTile / kRowsPerLoad / 4;
-    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
 #pragma unroll
-    for (uint32_t q = 0; q < kLoads; ++q) {
-        const uint32_t at = wave * kLoads + q;
-        const uint32_t row = at * kRowsPerLoad + lane / kPieces;
-        const uint32_t piece = (lane % kPieces) ^ swizzle<kRowBytes>(row);
+    for (uint32_t q = 0; q < kBytes / 1024 / kWaves; ++q) {
+        const uint32_t at = (wave * (kBytes / 1024 / kWaves) + q) * 1024;
         __builtin_amdgcn_global_load_lds(
-            reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(
-                reinterpret_cast<uintptr_t>(g + static_cast<uint64_t>(row) * stride + piece * 16)),
-            (__attribute__((address_space(3))) uint32_t*)(lds + at * 1024), 16, 0, 0);
+            reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(reinterpret_cast<uintptr_t>(g + at + lane * 16)),
+            (__attribute__((address_space(3))) uint32_t*)(lds + at), 16, 0, 0);
     }
 }
 
-template <int kRowBytes>
-__device__ __forceinline__ f16x8 fragment(const char* lds, uint32_t row, uint32_t piece)
+// Fragments of a stage: at LDS addresses a0 and a1 four or two of them
+// each, kA bytes apart, likewise two at b0 (and b1).  The reads and
+// the wait for them are one asm block, because the compiler would put a wait
+// for the loads of later stages (which go to other buffers) before reads of
+// LDS that it sees.
+template <int kA, int kB>
+__device__ __forceinline__ void read_4_2(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1, f16x8 (&fa)[2][4], f16x8 (&fb)[2][2])
 {
-    return *reinterpret_cast<const f16x8*>(lds + row * kRowBytes + ((piece ^ swizzle<kRowBytes>(row)) * 16));
+    asm volatile("ds_read_b128 %0, %12\n\tds_read_b128 %8, %14\n\tds_read_b128 %9, %14 offset:%17\n\t"
+                 "ds_read_b128 %1, %12 offset:%16\n\tds_read_b128 %2, %12 offset:2*%16\n\tds_read_b128 %3, %12 offset:3*%16\n\t"
+                 "ds_read_b128 %10, %15\n\tds_read_b128 %11, %15 offset:%17\n\t"
+                 "ds_read_b128 %4, %13\n\tds_read_b128 %5, %13 offset:%16\n\t"
+                 "ds_read_b128 %6, %13 offset:2*%16\n\tds_read_b128 %7, %13 offset:3*%16\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(fa[0][0]), "=&v"(fa[0][1]), "=&v"(fa[0][2]), "=&v"(fa[0][3]), "=&v"(fa[1][0]), "=&v"(fa[1][1]),
+                   "=&v"(fa[1][2]), "=&v"(fa[1][3]), "=&v"(fb[0][0]), "=&v"(fb[0][1]), "=&v"(fb[1][0]), "=&v"(fb[1][1])
+                 : "v"(a0), "v"(a1), "v"(b0), "v"(b1), "n"(kA), "n"(kB)
+                 : "memory");
+}
+
+template <int kA, int kB>
+__device__ __forceinline__ void read_4_1(uint32_t a0, uint32_t a1, uint32_t b0, f16x8 (&fa)[2][4], f16x8 (&fb)[1][2])
+{
+    asm volatile("ds_read_b128 %0, %10\n\tds_read_b128 %8, %12\n\tds_read_b128 %9, %12 offset:%14\n\t"
+                 "ds_read_b128 %1, %10 offset:%13\n\tds_read_b128 %2, %10 offset:2*%13\n\tds_read_b128 %3, %10 offset:3*%13\n\t"
+                 "ds_read_b128 %4, %11\n\tds_read_b128 %5, %11 offset:%13\n\t"
+                 "ds_read_b128 %6, %11 offset:2*%13\n\tds_read_b128 %7, %11 offset:3*%13\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(fa[0][0]), "=&v"(fa[0][1]), "=&v"(fa[0][2]), "=&v"(fa[0][3]), "=&v"(fa[1][0]), "=&v"(fa[1][1]),
+                   "=&v"(fa[1][2]), "=&v"(fa[1][3]), "=&v"(fb[0][0]), "=&v"(fb[0][1])
+                 : "v"(a0), "v"(a1), "v"(b0), "n"(kA), "n"(kB)
+                 : "memory");
+}
+
+template <int kA, int kB>
+__device__ __forceinline__ void read_2_2(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1, f16x8 (&fa)[2][2], f16x8 (&fb)[2][2])
+{
+    asm volatile("ds_read_b128 %0, %8\n\tds_read_b128 %4, %10\n\tds_read_b128 %5, %10 offset:%13\n\tds_read_b128 %1, %8 offset:%12\n\t"
+                 "ds_read_b128 %6, %11\n\tds_read_b128 %7, %11 offset:%13\n\tds_read_b128 %2, %9\n\tds_read_b128 %3, %9 offset:%12\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(fa[0][0]), "=&v"(fa[0][1]), "=&v"(fa[1][0]), "=&v"(fa[1][1]), "=&v"(fb[0][0]), "=&v"(fb[0][1]),
+                   "=&v"(fb[1][0]), "=&v"(fb[1][1])
+                 : "v"(a0), "v"(a1), "v"(b0), "v"(b1), "n"(kA), "n"(kB)
+                 : "memory");
+}
+
+template <int kA, int kB>
+__device__ __forceinline__ void read_2_1(uint32_t a0, uint32_t a1, uint32_t b0, f16x8 (&fa)[2][2], f16x8 (&fb)[1][2])
+{
+    asm volatile("ds_read_b128 %0, %6\n\tds_read_b128 %4, %8\n\tds_read_b128 %5, %8 offset:%10\n\tds_read_b128 %1, %6 offset:%9\n\t"
+                 "ds_read_b128 %2, %7\n\tds_read_b128 %3, %7 offset:%9\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(fa[0][0]), "=&v"(fa[0][1]), "=&v"(fa[1][0]), "=&v"(fa[1][1]), "=&v"(fb[0][0]), "=&v"(fb[0][1])
+                 : "v"(a0), "v"(a1), "v"(b0), "n"(kA), "n"(kB)
+                 : "memory");
+}
+
+// Meetings of a workgroup's waves.  A wave's loads to LDS, or its reads of LDS,
+// are waited for where the others go on to read, or overwrite, what they
+// touch.  The empty asm keeps memory accesses on their side.
+__device__ __forceinline__ void meet()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" : : : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" : : : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Until at most kLeft loads of this wave are on their way, and its reads of
+// LDS are done.
+template <int kLeft>
+__device__ __forceinline__ void wait_loads()
+{
+    static_assert(kLeft < 16, "the count's low bits");
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" : : : "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070 | kLeft);   // vmcnt(kLeft) lgkmcnt(0)
+}
+
+template <int kLeft>
+__device__ __forceinline__ void wait_loads_and_meet()
+{
+    wait_loads<kLeft>();
+    meet();
 }
 
 enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
 
 struct ProductArgs {
     const NsMat* tab;
-    uint32_t n, tiles;
+    float* parts;        // sums of the parts, [unit][kT * kT]
+    uint32_t* counters;  // finished parts, per tile of the launch; zero between launches
+    uint32_t n;
     uint32_t turn;       // which transpose of X is read
+    uint32_t depth;      // stages per part
     double a, b, c;      // coefficients of the step (kPoly)
     int lowered, lower;  // by how much the steps before and this one lower e
 };
 
 __device__ __forceinline__ int left_of(int e, int lowered) { return e > lowered ? e - lowered : 0; }
 
-// Value (row, c) of an operand, times kNsScale.
-template <int kTerms>
-__device__ __forceinline__ float get_term(const char* base, uint64_t row, uint64_t ld, uint32_t c)
+// Tile number k of the tiles on and under the diagonal of tm x tm, in bands
+// of four rows, down the columns of a band: tiles near each other in this
+// order share their operands' rows.
+__device__ __forceinline__ void lower_tile(uint32_t k, uint32_t tm, uint32_t& ti, uint32_t& tj)
 {
-    if (kTerms == 1) return static_cast<float>(*reinterpret_cast<const _Float16*>(base + (row * ld + c) * 2));
-    const char* p = base + (row * ld + (c & ~31u)) * 4 + (c & 31u) * 2;
-    return static_cast<float>(*reinterpret_cast<const _Float16*>(p)) + static_cast<float>(*reinterpret_cast<const _Float16*>(p + 64));
+    // band g starts at 8 g^2 + 2 g
+    uint32_t g = static_cast<uint32_t>((sqrtf(1.0f + 8.0f * static_cast<float>(k)) - 1.0f) * 0.125f);
+    while (8 * g * g + 2 * g > k) --g;
+    while (8 * (g + 1) * (g + 1) + 2 * (g + 1) <= k) ++g;
+    uint32_t at = k - (8 * g * g + 2 * g), left = tm - 4 * g < 4 ? tm - 4 * g : 4;
+    const uint32_t whole = left * (4 * g + 1);   // columns up to the band's first row
+    if (at < whole) {
+        tj = at / left;
+        ti = 4 * g + at % left;
+        return;
+    }
+    at -= whole;
+    tj = 4 * g + 1;
+    for (--left; at >= left; --left, ++tj) at -= left;
+    ti = tj + at;
 }
 
-template <int kTermsA, int kTermsB, int kKind, int kGramTerms>
-__global__ void __launch_bounds__(256, 2) ns_product_kernel(const ProductArgs args)
+// Tile number k of tn x tm, in bands of four rows, down the columns of a band.
+__device__ __forceinline__ void band_tile(uint32_t k, uint32_t tn, uint32_t tm, uint32_t& ti, uint32_t& tj)
 {
-    constexpr int kValues = (kTermsA == 1 && kTermsB == 1) ? 64 : 32;   // of the summed index per stage
-    constexpr int kRowA = kValues * 2 * kTermsA, kRowB = kValues * 2 * kTermsB;
-    constexpr uint32_t kStage = kNsTile * (kRowA + kRowB);
-    constexpr uint32_t kLds = 2 * kStage > kNsTile * kPitch * 4 ? 2 * kStage : kNsTile * kPitch * 4;
-    __shared__ __attribute__((aligned(128))) char lds[kLds];
+    const uint32_t g = k / (4 * tm), at = k - g * 4 * tm, left = tn - 4 * g < 4 ? tn - 4 * g : 4;
+    tj = at / left;
+    ti = 4 * g + at % left;
+}
 
-    // consecutive tiles go to one XCD (workgroups go round the eight in turn)
-    const uint32_t per = (args.tiles + 7) / 8;
-    const uint32_t t = (blockIdx.x & 7u) * per + (blockIdx.x >> 3);
-    if (t >= args.tiles || (blockIdx.x >> 3) >= per) return;
-    const uint32_t mi = kKind <= kPoly ? find_mat<&NsMat::sym0>(args.tab, args.n, t) : find_mat<&NsMat::apply0>(args.tab, args.n, t);
+template <int kT, int kTermsA, int kTermsB, int kKind, int kGramTerms>
+__global__ void __launch_bounds__(kT == 128 ? 256 : 512, 2) ns_product_kernel(const ProductArgs args)
+{
+    constexpr int kWaves = kT == 128 ? 4 : 8, kThreads = kWaves * 64;
+    constexpr int kWm = kT / 2, kWn = 64, kX = kWm / 32, kY = kWn / 32;   // a wave's part, in matrix-core tiles
+    constexpr int kValues = (kTermsA == 1 && kTermsB == 1) ? 32 : 16;     // of the summed index per stage
+    constexpr int kRowA = 32 * kTermsA, kRowB = 32 * kTermsB;             // bytes of a row in a block
+    constexpr uint32_t kStageA = kT * 2 * kValues * kTermsA, kStageB = kT * 2 * kValues * kTermsB, kStage = kStageA + kStageB;
+    constexpr int kRing = 4, kLoads = kStage / 1024 / kWaves;             // loads of a wave per stage
+    constexpr uint32_t kPitch = kT + 1, kStrip = 128;                     // of the result tile in LDS
+    constexpr uint32_t kLds = kRing * kStage > kStrip * kPitch * 4 ? kRing * kStage : kStrip * kPitch * 4;
+    __shared__ __attribute__((aligned(128))) char lds[kLds];
+    __shared__ uint32_t last_part;
+
+    const uint32_t mi = kKind <= kPoly ? (kKind == kGram ? find_mat<&NsMat::gram0>(args.tab, args.n, blockIdx.x)
+                                                         : find_mat<&NsMat::poly0>(args.tab, args.n, blockIdx.x))
+                                       : find_mat<&NsMat::apply0>(args.tab, args.n, blockIdx.x);
     const NsMat m = load_mat(args.tab, mi);
     const NsWork w = ns_work(m.mp, m.np, kGramTerms);
-    uint32_t ti, tj;
-    if (kKind <= kPoly) {
-        const uint32_t k = t - m.sym0;
-        ti = static_cast<uint32_t>((sqrtf(8.0f * static_cast<float>(k) + 1.0f) - 1.0f) * 0.5f);
-        while (ti * (ti + 1) / 2 > k) --ti;
-        while ((ti + 1) * (ti + 2) / 2 <= k) ++ti;
-        tj = k - ti * (ti + 1) / 2;
-    } else {
-        const uint32_t k = t - m.apply0, across = m.mp / kNsTile;
-        ti = k / across;
-        tj = k % across;
-    }
     const char* a;
     const char* b;
-    uint32_t depth;
+    uint32_t depth, first, tiles;
+    const uint32_t tm = m.mp / kT, tn = m.np / kT;
     if (kKind == kGram) {
         a = b = m.work + w.x;
         depth = m.np;
+        first = m.gram0;
+        tiles = tm * (tm + 1) / 2;
     } else if (kKind == kPoly) {
         a = b = m.work + w.s;
         depth = m.mp;
+        first = m.poly0;
+        tiles = tm * (tm + 1) / 2;
     } else {
         a = m.work + ((args.turn & 1u) ? w.xt[1] : w.xt[0]);
         b = m.work + w.p;
         depth = m.mp;
+        first = m.apply0;
+        tiles = tm * tn;
     }
-    const uint32_t i0 = ti * kNsTile, j0 = tj * kNsTile;
-    const uint32_t stride_a = depth * 2 * kTermsA, stride_b = depth * 2 * kTermsB;   // sides below 2^29
-    a += static_cast<uint64_t>(i0) * stride_a;
-    b += static_cast<uint64_t>(j0) * stride_b;
+    const uint32_t stages = depth / kValues, parts = (stages + args.depth - 1) / args.depth;
+    // a matrix has a multiple of eight workgroups, which go round the eight
+    // XCDs in turn; consecutive units of a matrix go to one XCD, neighbouring
+    // tiles of the same part, which share rows
+    const uint32_t units = tiles * parts, per = (units + 7) / 8, at = blockIdx.x - first;
+    const uint32_t unit = (at & 7u) * per + (at >> 3);
+    if (unit >= units) return;
+    const uint32_t k = unit % tiles, part = unit / tiles;
+    uint32_t ti, tj;
+    if (kKind <= kPoly) lower_tile(k, tm, ti, tj);
+    else band_tile(k, tn, tm, ti, tj);
+    const uint32_t i0 = ti * kT, j0 = tj * kT;
+    const uint32_t s0 = part * args.depth, s1 = s0 + args.depth < stages ? s0 + args.depth : stages;
+    a += static_cast<uint64_t>(ti) * stages * kStageA;
+    b += static_cast<uint64_t>(tj) * stages * kStageB;
 
-    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-    const uint32_t wi = (wave >> 1) * 64, wj = (wave & 1u) * 64;
-    f32x16 acc[2][2];
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t wave = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)));
+    const uint32_t wi = (kT == 128 ? wave >> 1 : wave >> 2) * kWm, wj = (kT == 128 ? wave & 1u : wave & 3u) * kWn;
+    f32x16 acc[kX][kY];
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < kX; ++x)
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < kY; ++y)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.0f;
 
-    const uint32_t stages = depth / kValues;
-    load_stage<kRowA>(a, stride_a, lds);
-    load_stage<kRowB>(b, stride_b, lds + kNsTile * kRowA);
-    __syncthreads();
-    for (uint32_t s = 0; s < stages; ++s) {
-        const char* now = lds + (s & 1u) * kStage;
-        if (s + 1 < stages) {
-            char* next = lds + ((s + 1) & 1u) * kStage;
-            load_stage<kRowA>(a + (s + 1) * kRowA, stride_a, next);
-            load_stage<kRowB>(b + (s + 1) * kRowB, stride_b, next + kNsTile * kRowA);
+    // stage s (the last one again behind the end, so that the waits count alike)
+    auto load_a = [&](uint32_t s) {
+        load_stage<kWaves, kStageA>(a + static_cast<uint64_t>(s < s1 ? s : s1 - 1) * kStageA, lds + (s % kRing) * kStage, wave, lane);
+    };
+    auto load_b = [&](uint32_t s) {
+        load_stage<kWaves, kStageB>(b + static_cast<uint64_t>(s < s1 ? s : s1 - 1) * kStageB, lds + (s % kRing) * kStage + kStageA, wave, lane);
+    };
+    // A stage is 16 values of two-term operands, whose second fragments are
+    // the l terms, or 32 values of one-term operands, whose second fragments
+    // are the second block.  A fragment is 32 rows by 16 values, eight per lane.
+    constexpr int kNb = kTermsA == kTermsB ? 2 : 1;
+    f16x8 fa[2][kX], fb[kNb][kY];
+    const uint32_t row_a = wi + (lane & 31u), row_b = wj + (lane & 31u);
+    // (the rows of a wave's other fragments are multiples of 32 further on: the same swizzle)
+    const uint32_t pa = (lane >> 5) ^ swizzle<kTermsA>(row_a), pb = (lane >> 5) ^ swizzle<kTermsB>(row_b);
+    const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
+    const uint32_t at_a = lds0 + row_a * kRowA + pa * 16, at_b = lds0 + kStageA + row_b * kRowB + pb * 16;
+    const uint32_t at_a1 = kTermsA == 2 ? lds0 + row_a * kRowA + (pa ^ 2u) * 16 : at_a + kT * kRowA;
+    const uint32_t at_b1 = kTermsB == 2 ? lds0 + kStageA + row_b * kRowB + (pb ^ 2u) * 16 : at_b + kT * kRowB;
+    auto read = [&](uint32_t s) {
+        const uint32_t now = (s % kRing) * kStage;
+        if constexpr (kNb == 2) {
+            if constexpr (kX == 4) read_4_2<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, now + at_b1, fa, fb);
+            else read_2_2<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, now + at_b1, fa, fb);
+        } else {
+            if constexpr (kX == 4) read_4_1<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, fa, fb);
+            else read_2_1<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, fa, fb);
         }
+    };
+    auto product = [&](const f16x8 (&x8)[kX], const f16x8 (&y8)[kY]) {
 #pragma unroll
-        for (uint32_t kk = 0; kk < kValues / 16; ++kk) {
-            f16x8 fa[2][kTermsA], fb[2][kTermsB];
+        for (int x = 0; x < kX; ++x)
 #pragma unroll
-            for (uint32_t x = 0; x < 2; ++x) {
+            for (int y = 0; y < kY; ++y) acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x8[x], y8[y], acc[x][y], 0, 0, 0);
+    };
+    // Multiply what has been read; in between, while the matrix cores are
+    // busy, send for stage s.  Sent for beside the reads of LDS, the loads held
+    // those up: the matrix cores were busy 58% of the time against 78% now,
+    // the product of 8192 x 8192 and 8192 x 28672 took 10.0 against 8.6 ms.
+    auto multiply = [&](uint32_t s) {
+        product(fa[0], fb[0]);
+        __builtin_amdgcn_sched_barrier(0);
+        load_a(s);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (kTermsA == 1) {
+            load_b(s);
+            __builtin_amdgcn_sched_barrier(0);
+            product(fa[1], fb[1]);                               // the second 16 values
+        } else {
+            if constexpr (kTermsB == 2) product(fa[0], fb[1]);   // h l
+            __builtin_amdgcn_sched_barrier(0);
+            load_b(s);
+            __builtin_amdgcn_sched_barrier(0);
+            product(fa[1], fb[0]);                               // l h
+        }
+    };
 #pragma unroll
-                for (uint32_t p = 0; p < kTermsA; ++p)
-                    fa[x][p] = fragment<kRowA>(now, wi + x * 32 + (lane & 31u), p * 4 + kk * 2 + (lane >> 5));
+    for (uint32_t s = 0; s < 3; ++s) {
+        load_a(s0 + s);
+        load_b(s0 + s);
+    }
+    if (kT == 128) {
+        for (uint32_t s = s0; s < s1; ++s) {
+            wait_loads_and_meet<2 * kLoads>();   // stage s is here, stage s - 1 has been read
+            read(s);
+            multiply(s + 3);
+        }
+    } else {
+        // Two waves share a SIMD.  Waves 4 to 7 run one meeting behind waves 0
+        // to 3, so that of the two one reads LDS while the other multiplies:
+        // between two meetings a wave does one of the two for a stage.  A
+        // buffer is loaded anew once both groups have read it; a stage has
+        // arrived before the first group meets to read it.
+        const bool second = wave >= 4;
+        wait_loads_and_meet<2 * kLoads>();
+        if (second) meet();
+        for (uint32_t s = s0; s < s1; ++s) {
+            read(s);
+            if (second) wait_loads<kLoads>();
+            meet();
+            __builtin_amdgcn_s_setprio(1);
+            multiply(s + 3);
+            __builtin_amdgcn_s_setprio(0);
+            if (!second) wait_loads<2 * kLoads>();
+            meet();
+        }
+        if (!second) meet();
+    }
+    wait_loads_and_meet<0>();
+
+    if (parts > 1) {
+        // This part's sums, in the registers' own order.  They go past the
+        // XCD's L2 (device-scope stores and loads of 8 bytes): a fence that
+        // writes the L2 back costs tens of microseconds here.
+        typedef unsigned long long u64;
+        u64* mine = reinterpret_cast<u64*>(args.parts) + (static_cast<uint64_t>(first) + unit) * (kT * kT / 2) + threadIdx.x;
 #pragma unroll
-                for (uint32_t p = 0; p < kTermsB; ++p)
-                    fb[x][p] = fragment<kRowB>(now + kNsTile * kRowA, wj + x * 32 + (lane & 31u), p * 4 + kk * 2 + (lane >> 5));
-            }
+        for (int x = 0; x < kX; ++x)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int y = 0; y < kY; ++y)
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[x][0], fb[y][0], acc[x][y], 0, 0, 0);
-                    if (kTermsB == 2) acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[x][0], fb[y][kTermsB - 1], acc[x][y], 0, 0, 0);
-                    if (kTermsA == 2) acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[x][kTermsA - 1], fb[y][0], acc[x][y], 0, 0, 0);
+                for (int q = 0; q < 8; ++q) {
+                    const u64 v = static_cast<u64>(__float_as_uint(acc[x][y][2 * q])) |
+                                  (static_cast<u64>(__float_as_uint(acc[x][y][2 * q + 1])) << 32);
+                    __hip_atomic_store(mine + ((x * kY + y) * 8 + q) * kThreads, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
                 }
+        wait_loads_and_meet<0>();   // of every wave, its stores have reached memory
+        if (threadIdx.x == 0) {
+            uint32_t* counter = args.counters + first + k;
+            const uint32_t done = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            last_part = done == parts - 1;
+            // for the next launch; nobody counts this tile any more
+            if (done == parts - 1) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
         __syncthreads();
+        if (!last_part) return;
+        u64* all = mine - static_cast<uint64_t>(part) * tiles * (kT * kT / 2);
+#pragma unroll
+        for (int x = 0; x < kX; ++x)
+#pragma unroll
+            for (int y = 0; y < kY; ++y)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.0f;
+        for (uint32_t p = 0; p < parts; ++p) {
+            u64* from = all + static_cast<uint64_t>(p) * tiles * (kT * kT / 2);
+#pragma unroll
+            for (int x = 0; x < kX; ++x)
+#pragma unroll
+                for (int y = 0; y < kY; ++y) {
+                    u64 v[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        v[q] = __hip_atomic_load(from + ((x * kY + y) * 8 + q) * kThreads, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        acc[x][y][2 * q] += __uint_as_float(static_cast<uint32_t>(v[q]));
+                        acc[x][y][2 * q + 1] += __uint_as_float(static_cast<uint32_t>(v[q] >> 32));
+                    }
+                }
+        }
     }
 
-    // the tile through LDS, values times kNsScale (products carry its square)
-    float* tile = reinterpret_cast<float*>(lds);
+    // the tile through LDS, values times kNsScale (products carry its
+    // square), kStrip rows at a time
     float unscale = 1.0f / kNsScale, ca = 0.0f, cb = 0.0f, cc = 0.0f;
     if (kKind == kPoly || kKind == kLast) {
         const int e0 = reinterpret_cast<const NsScaling*>(m.work + w.inv)->e;
@@ -432,58 +668,80 @@ __global__ void __launch_bounds__(256, 2) ns_product_kernel(const ProductArgs ar
         cb = static_cast<float>(ldexp(args.b, up - 2 * before));
         cc = static_cast<float>(ldexp(args.c, up - 4 * before));
     }
+    float* tile = reinterpret_cast<float*>(lds);
+    for (uint32_t strip = 0; strip < kT; strip += kStrip) {
+        __syncthreads();   // the stages, or the strip before, have been read
+        if (wi / kStrip * kStrip == strip) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < kX; ++x)
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+                for (int y = 0; y < kY; ++y)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const uint32_t i = wi + x * 32 + 8 * (e / 4) + 4 * (lane >> 5) + (e & 3);
-                const uint32_t j = wj + y * 32 + (lane & 31u);
-                float v = acc[x][y][e] * unscale;
-                if (kKind == kPoly) {
-                    const float sv = get_term<kGramTerms>(m.work + w.s, i0 + i, m.mp, j0 + j);
-                    v = fmaf(cc, v, cb * sv);
-                    if (i0 + i == j0 + j) v += ca * kNsScale;
-                }
-                tile[i * kPitch + j] = v;
-            }
-    __syncthreads();
-
-    if (kKind == kLast) {
-        // D is X'^T: element (i, j) is X'(j, i); rows of the natural matrix
-        // are i if tall, else j
-        const bool tall = (m.flags & kNsTall) != 0;
-        const uint32_t r0 = tall ? i0 : j0, c0 = tall ? j0 : i0;
-        for (uint32_t v = threadIdx.x; v < kNsTile * kNsTile; v += 256) {
-            const uint32_t r = v / kNsTile, c = v % kNsTile;
-            if (r0 + r < m.rows && c0 + c < m.cols) put_result(m, r0 + r, c0 + c, tall ? tile[r * kPitch + c] : tile[c * kPitch + r]);
+                    for (int e = 0; e < 16; ++e) {
+                        const uint32_t i = wi + x * 32 + 8 * (e / 4) + 4 * (lane >> 5) + (e & 3);
+                        const uint32_t j = wj + y * 32 + (lane & 31u);
+                        tile[(i - strip) * kPitch + j] = acc[x][y][e] * unscale;
+                    }
         }
-        return;
-    }
-    char* out_rows;      // takes D
-    char* out_cols;      // takes D transposed
-    uint64_t ld_rows, ld_cols;
-    if (kKind == kApply) {
-        out_rows = m.work + ((args.turn & 1u) ? w.xt[0] : w.xt[1]);
-        out_cols = m.work + w.x;
-        ld_rows = m.mp;
-        ld_cols = m.np;
-    } else {
-        out_rows = out_cols = m.work + (kKind == kGram ? w.s : w.p);
-        ld_rows = ld_cols = m.mp;
-    }
-    for (uint32_t v = threadIdx.x; v < kNsTile * kNsTile / 8; v += 256) {
-        const uint32_t r = v / (kNsTile / 8), c = v % (kNsTile / 8) * 8;
-        float d[8];
+        __syncthreads();
+        const uint32_t is = i0 + strip;   // row of D that the strip starts at
+
+        if (kKind == kLast) {
+            // D is X'^T: element (i, j) is X'(j, i); rows of the natural
+            // matrix are i if tall, else j
+            if (m.flags & kNsTall) {
+                for (uint32_t v = threadIdx.x; v < kStrip * kT; v += kThreads) {
+                    const uint32_t r = v / kT, c = v % kT;
+                    if (is + r < m.rows && j0 + c < m.cols) put_result(m, is + r, j0 + c, tile[r * kPitch + c]);
+                }
+            } else {
+                for (uint32_t v = threadIdx.x; v < kStrip * kT; v += kThreads) {
+                    const uint32_t r = v / kStrip, c = v % kStrip;
+                    if (j0 + r < m.rows && is + c < m.cols) put_result(m, j0 + r, is + c, tile[c * kPitch + r]);
+                }
+            }
+            continue;
+        }
+        char* out_rows;      // takes D
+        char* out_cols;      // takes D transposed
+        uint32_t ld_rows, ld_cols;
+        if (kKind == kApply) {
+            out_rows = m.work + ((args.turn & 1u) ? w.xt[0] : w.xt[1]);
+            out_cols = m.work + w.x;
+            ld_rows = m.mp;
+            ld_cols = m.np;
+        } else {
+            out_rows = out_cols = m.work + (kKind == kGram ? w.s : w.p);
+            ld_rows = ld_cols = m.mp;
+        }
+        // a I + b S + c S^2 from S^2, at elements (row, c .. c + 7)
+        auto polynomial = [&](uint32_t row, uint32_t c, float (&d)[8]) {
+            float sv[8];
+            get_terms<kT, kGramTerms>(m.work + w.s, row, m.mp, c, sv);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] = tile[r * kPitch + c + e];
-        if (kKind == kApply) put_terms<2>(out_rows, i0 + r, ld_rows, j0 + c, d);
-        else put_terms<kGramTerms>(out_rows, i0 + r, ld_rows, j0 + c, d);
-        if (kKind == kApply || ti != tj) {
+            for (int e = 0; e < 8; ++e) {
+                d[e] = fmaf(cc, d[e], cb * sv[e]);
+                if (row == c + e) d[e] += ca * kNsScale;
+            }
+        };
+        // two lanes per row of a block
+        for (uint32_t v = threadIdx.x; v < kStrip * kT / 8; v += kThreads) {
+            float d[8];
+            {
+                const uint32_t c = (v & 1u) * 8 + v / (kStrip * 2) * 16, r = (v >> 1) % kStrip;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = tile[(c + e) * kPitch + r];
-            put_terms<kGramTerms>(out_cols, j0 + r, ld_cols, i0 + c, d);
+                for (int e = 0; e < 8; ++e) d[e] = tile[r * kPitch + c + e];
+                if (kKind == kPoly) polynomial(is + r, j0 + c, d);
+                if (kKind == kApply) put_terms<kT, 2>(out_rows, is + r, ld_rows, j0 + c, d);
+                else put_terms<kT, kGramTerms>(out_rows, is + r, ld_rows, j0 + c, d);
+            }
+            if (kKind == kApply || ti != tj) {
+                const uint32_t c = (v & 1u) * 8 + v / (kT * 2) * 16, r = (v >> 1) % kT;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) d[e] = tile[(c + e) * kPitch + r];
+                if (kKind == kPoly) polynomial(j0 + r, is + c, d);
+                put_terms<kT, kGramTerms>(out_cols, j0 + r, ld_cols, is + c, d);
+            }
         }
     }
 }
@@ -659,18 +917,20 @@ hipError_t launch_small(const NsCall& c, const NsMat* tab, uint32_t n, uint32_t 
     return hipGetLastError();
 }
 
-template <int kGramTerms>
+template <int kT, int kGramTerms>
 hipError_t launch_big(const NsCall& c, const NsMat* tab, hipStream_t s)
 {
     const uint32_t n = c.nbig;
-    hipLaunchKernelGGL(ns_norm_kernel, dim3(c.prep_tiles), dim3(256), 0, s, tab, n, c.gram_terms);
+    hipLaunchKernelGGL(ns_norm_kernel, dim3(c.prep_tiles), dim3(256), 0, s, tab, n, c.gram_terms, c.counters, c.ncounters);
     hipLaunchKernelGGL(ns_scale_kernel, dim3(n), dim3(1024), 0, s, tab, c.gram_terms, c.eps);
-    hipLaunchKernelGGL(ns_split_kernel, dim3(c.prep_tiles), dim3(256), 0, s, tab, n, c.gram_terms);
-    const dim3 sym((c.sym_tiles + 7) / 8 * 8), apply((c.apply_tiles + 7) / 8 * 8), threads(256);
+    hipLaunchKernelGGL((ns_split_kernel<kT, kGramTerms>), dim3(c.prep_tiles), dim3(256), 0, s, tab, n);
+    const dim3 threads(kT == 128 ? 256 : 512);
     int lowered = 0;
     for (uint32_t k = 0; k < c.steps; ++k) {
         ProductArgs args{};
         args.tab = tab;
+        args.parts = c.parts;
+        args.counters = c.counters;
         args.n = n;
         args.turn = k;
         args.a = c.coef[3 * k];
@@ -679,14 +939,15 @@ hipError_t launch_big(const NsCall& c, const NsMat* tab, hipStream_t s)
         args.lowered = lowered;
         args.lower = static_cast<int>(c.shift[k]);
         lowered += args.lower;
-        args.tiles = c.sym_tiles;
-        hipLaunchKernelGGL((ns_product_kernel<kGramTerms, kGramTerms, kGram, kGramTerms>), sym, threads, 0, s, args);
-        hipLaunchKernelGGL((ns_product_kernel<kGramTerms, kGramTerms, kPoly, kGramTerms>), sym, threads, 0, s, args);
-        args.tiles = c.apply_tiles;
+        args.depth = c.gram.depth;
+        hipLaunchKernelGGL((ns_product_kernel<kT, kGramTerms, kGramTerms, kGram, kGramTerms>), dim3(c.gram.units), threads, 0, s, args);
+        args.depth = c.poly.depth;
+        hipLaunchKernelGGL((ns_product_kernel<kT, kGramTerms, kGramTerms, kPoly, kGramTerms>), dim3(c.poly.units), threads, 0, s, args);
+        args.depth = c.apply.depth;
         if (k + 1 < c.steps)
-            hipLaunchKernelGGL((ns_product_kernel<2, kGramTerms, kApply, kGramTerms>), apply, threads, 0, s, args);
+            hipLaunchKernelGGL((ns_product_kernel<kT, 2, kGramTerms, kApply, kGramTerms>), dim3(c.apply.units), threads, 0, s, args);
         else
-            hipLaunchKernelGGL((ns_product_kernel<2, kGramTerms, kLast, kGramTerms>), apply, threads, 0, s, args);
+            hipLaunchKernelGGL((ns_product_kernel<kT, 2, kGramTerms, kLast, kGramTerms>), dim3(c.apply.units), threads, 0, s, args);
     }
     return hipGetLastError();
 }
@@ -715,7 +976,10 @@ int ns_launch(const NsCall& c, NsMat* device_table, void* stream)
                      : launch_small<32>(c, tab, c.nsmall[k], c.small_chunks[k], s);
         tab += c.nsmall[k];
     }
-    if (err == hipSuccess && c.nbig > 0) err = c.gram_terms == 1 ? launch_big<1>(c, tab, s) : launch_big<2>(c, tab, s);
+    if (err == hipSuccess && c.nbig > 0) {
+        if (c.tile == 256) err = c.gram_terms == 1 ? launch_big<256, 1>(c, tab, s) : launch_big<256, 2>(c, tab, s);
+        else err = c.gram_terms == 1 ? launch_big<128, 1>(c, tab, s) : launch_big<128, 2>(c, tab, s);
+    }
     return err;
 }
 
