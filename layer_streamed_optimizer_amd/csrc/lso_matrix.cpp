@@ -2,7 +2,7 @@
 // plan and the table of a call.
 #include <algorithm>
 #include <cmath>
-#include <cstring>
+#include <cstdlib>
 #include <new>
 #include <vector>
 
@@ -78,6 +78,15 @@ lso_status check_params(const lso_ns_params* p, NsCall& c)
 // Bytes from the first to the last element of rows x cols at stride ld.
 uint64_t span(uint64_t rows, uint64_t cols, uint64_t ld, uint64_t elem) { return ((rows - 1) * ld + cols) * elem; }
 
+// kNsQuads if the matrix may be read and written four columns at a time.
+uint32_t quads(const NsMat& m, uint64_t cols)
+{
+    auto fits = [](const void* p, uint64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
+    const bool ok = cols % 4 == 0 && m.ld_src % 4 == 0 && m.ld_dst % 4 == 0 && fits(m.src, (m.flags & kNsSrcF32) ? 16 : 8) &&
+                    fits(m.dst, (m.flags & kNsDstF32) ? 16 : 8) && fits(m.m, 16) && fits(m.master, 16);
+    return ok ? kNsQuads : 0;
+}
+
 lso_status check_sides(uint64_t rows, uint64_t cols, size_t i)
 {
     if (rows > kMaxSide || cols > kMaxSide) return fail(LSO_E_INVALID, "matrix %zu: a side is too large", i);
@@ -129,6 +138,7 @@ lso_status collect(const lso_matrix* mats, size_t n, std::vector<Item>& items, s
         it.mat.ld_src = static_cast<uint32_t>(a.ld_x);
         it.mat.ld_dst = static_cast<uint32_t>(a.ld_y);
         it.mat.flags = (a.x_dtype == LSO_DT_F32 ? kNsSrcF32 : 0) | (a.y_dtype == LSO_DT_F32 ? kNsDstF32 : 0);
+        it.mat.flags |= quads(it.mat, it.cols);
         items.push_back(it);
     }
     return LSO_OK;
@@ -183,6 +193,7 @@ lso_status collect(const lso_muon_block* blocks, size_t n, std::vector<Item>& it
         it.mat.step = static_cast<float>(-b.lr * b.scale);
         if (!std::isfinite(it.mat.keep) || !std::isfinite(it.mat.step))
             return fail(LSO_E_INVALID, "matrix %zu: lr * weight_decay or lr * scale is not an FP32 number", i);
+        it.mat.flags |= quads(it.mat, it.cols);
         items.push_back(it);
     }
     return LSO_OK;
@@ -231,7 +242,8 @@ uint32_t tile_edge(const std::vector<Item>& items)
         const uint64_t k = std::min(it.rows, it.cols), l = std::max(it.rows, it.cols);
         if (small_class(k) < 0) tiles += padded(k, 256) / 256 * (padded(l, 256) / 256);
     }
-    return tiles >= 512 ? 256 : 128;
+    if (const char* e = std::getenv("NS_EDGE")) return std::atoi(e);
+    return tiles >= 512 ? 256 : tiles >= 256 ? 128 : 64;
 }
 
 // Order the items (small path by class, then the general path, deep matrices
@@ -249,7 +261,7 @@ uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<N
     });
     c.tile = tile_edge(items);
     const uint64_t edge = c.tile;
-    std::vector<Tiles> lists[3];
+    std::vector<Tiles> lists[4];
     uint64_t most_index = 0;
     for (int cls = 0; cls <= kNsClasses; ++cls) {
         uint64_t chunks = 0, prep = 0;
@@ -283,6 +295,7 @@ uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<N
                 lists[0].push_back({tm * (tm + 1) / 2, np / values});
                 lists[1].push_back({tm * (tm + 1) / 2, mp / values});
                 lists[2].push_back({tm * tn, mp / 16});
+                lists[3].push_back({tm * tn, mp / 32});
             }
             ++count;
             most_index = std::max({most_index, chunks, prep, uint64_t{count} * 4});
@@ -297,16 +310,16 @@ uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<N
         }
     }
     if (c.nbig > 0) {
-        NsProduct* products[3] = {&c.gram, &c.poly, &c.apply};
-        uint32_t NsMat::*firsts[3] = {&NsMat::gram0, &NsMat::poly0, &NsMat::apply0};
+        NsProduct* products[4] = {&c.gram, &c.poly, &c.apply, &c.apply_one};
+        uint32_t NsMat::*firsts[4] = {&NsMat::gram0, &NsMat::poly0, &NsMat::apply0, &NsMat::apply_one0};
         uint64_t most_units = 0, part_units = 0;
-        for (int p = 0; p < 3; ++p) {
+        for (int p = 0; p < 4; ++p) {
             const uint64_t units_before = units_of(lists[p], UINT32_MAX);
             if (units_before > kMaxIndex) {
                 most_index = units_before;
                 break;
             }
-            products[p]->depth = part_depth(lists[p], edge == 256 ? 256 : 512);
+            products[p]->depth = part_depth(lists[p], edge == 256 ? 256 : edge == 128 ? 512 : 1024);
             uint64_t units = 0;
             bool cut = false;
             NsMat* m = table.data() + (table.size() - c.nbig);

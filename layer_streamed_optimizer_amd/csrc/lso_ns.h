@@ -28,6 +28,7 @@ enum : uint32_t {
     kNsTall = 4u,       // rows > cols: the transpose is iterated on
     kNsMuon = 8u,       // update: src is the gradient, dst the weight (or null)
     kNsNesterov = 16u,
+    kNsQuads = 32u,     // groups of four columns are whole, and aligned in every array
 };
 
 // One matrix of a call (an entry of the table in the workspace).
@@ -48,14 +49,14 @@ struct NsMat {
     uint32_t gram0;     // units (tile, part of the summed index) of S, a multiple of 8 per matrix
     uint32_t poly0;     // of the polynomial
     uint32_t apply0;    // of X
-    uint32_t pad;
+    uint32_t apply_one0;   // of X where X^T has one term
 };
 static_assert(sizeof(NsMat) == 104, "NsMat layout");
 
 // Offsets of a general-path matrix inside its part of the workspace:
 // X (smaller side by larger, gram_terms FP16 numbers per value, read by the
-// product S = X X^T), its transpose twice (two numbers per value, read and
-// written in turn by the product with the polynomial P), S and P.
+// product S = X X^T), its transpose twice (up to two numbers per value, read
+// and written in turn by the product with the polynomial P), S and P.
 struct NsWork {
     uint64_t x, xt[2], s, p, partial, inv, bytes;
 };
@@ -97,8 +98,8 @@ struct NsCall {
     uint32_t nsmall[kNsClasses], nbig;
     uint32_t small_chunks[kNsClasses];     // index spaces
     uint32_t prep_tiles;
-    NsProduct gram, poly, apply;
-    uint32_t tile;                         // edge of a product tile: 128 or 256
+    NsProduct gram, poly, apply, apply_one;
+    uint32_t tile;                         // edge of a product tile: 64, 128 or 256
     float* parts;                          // workspace of the parts' sums
     uint32_t* counters;
     uint32_t ncounters;

@@ -30,25 +30,42 @@ namespace {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 #define LSO_CONST __attribute__((address_space(4)))
 
 // ------------------------------------------------------------- the table
 
-// Entries per writer launch: the kernel arguments stay under 4 KiB.
-constexpr uint32_t kWriteMats = 38;
+// Written by small kernels whose arguments carry the entries (nothing is read
+// from host memory later): 16 KiB of arguments at a time, or 2 KiB for the
+// few matrices of most calls.  308 matrices: two launches (5 us) against nine of
+// 4 KiB (20 us).
+template <uint32_t kCount>
 struct NsTablePart {
     NsMat* dst;
     uint32_t count;
     uint32_t pad;
-    NsMat src[kWriteMats];
+    NsMat src[kCount];
 };
-static_assert(sizeof(NsTablePart) <= 4000, "writer arguments");
+constexpr uint32_t kWriteFew = 19, kWriteMany = 157;
+static_assert(sizeof(NsTablePart<kWriteFew>) <= 2048 && sizeof(NsTablePart<kWriteMany>) <= 16384, "writer arguments");
 
-__global__ void __launch_bounds__(64) ns_table_kernel(const NsTablePart part)
+template <uint32_t kCount>
+__global__ void __launch_bounds__(64) ns_table_kernel(const NsTablePart<kCount> part)
 {
-    if (threadIdx.x < part.count) part.dst[threadIdx.x] = part.src[threadIdx.x];
+    const uint32_t i = blockIdx.x * 64 + threadIdx.x;
+    if (i < part.count) part.dst[i] = part.src[i];
+}
+
+template <uint32_t kCount>
+void write_table(NsMat* dst, const NsMat* src, uint32_t count, hipStream_t s)
+{
+    NsTablePart<kCount> part;
+    part.dst = dst;
+    part.count = count;
+    part.pad = 0;
+    for (uint32_t j = 0; j < kCount; ++j) part.src[j] = src[j < count ? j : 0];
+    hipLaunchKernelGGL(ns_table_kernel<kCount>, dim3((count + 63) / 64), dim3(64), 0, s, part);
 }
 
 __device__ __forceinline__ NsMat load_mat(const NsMat* tab, uint32_t i)
@@ -71,13 +88,20 @@ __device__ __forceinline__ uint32_t find_mat(const NsMat* tab, uint32_t n, uint3
 
 // ------------------------------------------------------ elements of u
 
-__device__ __forceinline__ float load_src(const NsMat& m, uint64_t r, uint32_t c)
+__device__ __forceinline__ float load_src(const NsMat& m, uint64_t i)
 {
-    const uint64_t i = r * m.ld_src + c;
     return (m.flags & kNsSrcF32) ? static_cast<const float*>(m.src)[i]
                                  : bf16_widen(static_cast<const uint16_t*>(m.src)[i]);
 }
 
+__device__ __forceinline__ f32x4 load_src4(const NsMat& m, uint64_t i)
+{
+    if (m.flags & kNsSrcF32) return *reinterpret_cast<const f32x4*>(static_cast<const float*>(m.src) + i);
+    const u32x2 h = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(m.src) + i);
+    return f32x4{bf16_widen(h.x & 0xFFFFu), bf16_widen(h.x >> 16), bf16_widen(h.y & 0xFFFFu), bf16_widen(h.y >> 16)};
+}
+
+// The new momentum of the old one m and the gradient g, and u of the new one.
 __device__ __forceinline__ float new_momentum(const NsMat& m, float old, float g) { return fmaf(m.beta, old, m.c1 * g); }
 
 __device__ __forceinline__ float lookahead(const NsMat& m, float m1, float g)
@@ -89,7 +113,7 @@ __device__ __forceinline__ float lookahead(const NsMat& m, float m1, float g)
 template <bool kFirst>
 __device__ __forceinline__ float load_u(const NsMat& m, uint32_t r, uint32_t c)
 {
-    const float g = load_src(m, r, c);
+    const float g = load_src(m, static_cast<uint64_t>(r) * m.ld_src + c);
     if (!(m.flags & kNsMuon)) return g;
     float* p = m.m + static_cast<uint64_t>(r) * m.cols + c;
     float m1 = *p;
@@ -98,6 +122,32 @@ __device__ __forceinline__ float load_u(const NsMat& m, uint32_t r, uint32_t c)
         *p = m1;
     }
     return lookahead(m, m1, g);
+}
+
+// u of elements (r, c .. c + 3), zeros outside the matrix.
+template <bool kFirst>
+__device__ __forceinline__ f32x4 load_u4(const NsMat& m, uint32_t r, uint32_t c)
+{
+    f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (r >= m.rows || c >= m.cols) return u;
+    if (m.flags & kNsQuads) {
+        const f32x4 g = load_src4(m, static_cast<uint64_t>(r) * m.ld_src + c);
+        if (!(m.flags & kNsMuon)) return g;
+        f32x4* p = reinterpret_cast<f32x4*>(m.m + static_cast<uint64_t>(r) * m.cols + c);
+        f32x4 m1 = *p;
+        if (kFirst) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m1[e] = new_momentum(m, m1[e], g[e]);
+            *p = m1;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = lookahead(m, m1[e], g[e]);
+        return u;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (c + e < m.cols) u[e] = load_u<kFirst>(m, r, c + e);
+    return u;
 }
 
 // y of element (r, c): stored, or applied to master and weight.
@@ -113,6 +163,42 @@ __device__ __forceinline__ void put_result(const NsMat& m, uint32_t r, uint32_t 
     const uint64_t i = static_cast<uint64_t>(r) * m.ld_dst + c;
     if (m.flags & kNsDstF32) static_cast<float*>(m.dst)[i] = o;
     else static_cast<uint16_t*>(m.dst)[i] = static_cast<uint16_t>(bf16_rne(o));
+}
+
+__device__ __forceinline__ u32x2 bf16_rne4(f32x4 v)
+{
+    return u32x2{bf16_rne(v.x) | (bf16_rne(v.y) << 16), bf16_rne(v.z) | (bf16_rne(v.w) << 16)};
+}
+
+// y of elements (r, c .. c + 3) as far as the matrix goes; old: their master
+// weights, read before (update, kNsQuads).
+__device__ __forceinline__ void put_result4(const NsMat& m, uint32_t r, uint32_t c, f32x4 o, f32x4 old)
+{
+    if (r >= m.rows || c >= m.cols) return;
+    if (!(m.flags & kNsQuads)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < m.cols) put_result(m, r, c + e, o[e]);
+        return;
+    }
+    if (m.flags & kNsMuon) {
+        const uint64_t i = static_cast<uint64_t>(r) * m.cols + c;
+        f32x4 p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = fmaf(m.step, o[e], m.keep * old[e]);
+        *reinterpret_cast<f32x4*>(m.master + i) = p;
+        if (m.dst) *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(m.dst) + i) = bf16_rne4(p);
+        return;
+    }
+    const uint64_t i = static_cast<uint64_t>(r) * m.ld_dst + c;
+    if (m.flags & kNsDstF32) *reinterpret_cast<f32x4*>(static_cast<float*>(m.dst) + i) = o;
+    else *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(m.dst) + i) = bf16_rne4(o);
+}
+
+__device__ __forceinline__ f32x4 old_master4(const NsMat& m, uint32_t r, uint32_t c)
+{
+    if ((m.flags & (kNsMuon | kNsQuads)) != (kNsMuon | kNsQuads) || r >= m.rows || c >= m.cols) return f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    return *reinterpret_cast<const f32x4*>(m.master + static_cast<uint64_t>(r) * m.cols + c);
 }
 
 // Sum over a workgroup of kN threads in a fixed order; valid in thread 0.
@@ -150,17 +236,15 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const NsMat* tab, uint32_t
     const NsMat m = load_mat(tab, i);
     uint32_t r0, c0;
     prep_tile(m, blockIdx.x - m.prep0, r0, c0);
-    const uint32_t c = c0 + (threadIdx.x & 63u);
+    const uint32_t c = c0 + (threadIdx.x & 15u) * 4, r = r0 + (threadIdx.x >> 4);
+    f32x4 u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) u[k] = load_u4<true>(m, r + 16 * k, c);
     double sum = 0.0;
-    if (c < m.cols) {
-#pragma unroll 4
-        for (uint32_t k = threadIdx.x >> 6; k < kNsPrep; k += 4) {
-            if (r0 + k < m.rows) {
-                const double u = load_u<true>(m, r0 + k, c);
-                sum = fma(u, u, sum);
-            }
-        }
-    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum = fma(static_cast<double>(u[k][e]), static_cast<double>(u[k][e]), sum);
     sum = group_sum<256>(sum);
     if (threadIdx.x == 0) {
         const NsWork w = ns_work(m.mp, m.np, gram_terms);
@@ -248,7 +332,7 @@ __device__ __forceinline__ void get_terms(const char* base, uint32_t row, uint32
 }
 
 // X_0 and its transpose from u, zeros in the padding.
-template <int kT, int kGramTerms>
+template <int kT, int kGramTerms, int kXTerms>
 __global__ void __launch_bounds__(256) ns_split_kernel(const NsMat* tab, uint32_t n)
 {
     __shared__ float tile[kNsPrep][kNsPrep + 1];
@@ -258,14 +342,15 @@ __global__ void __launch_bounds__(256) ns_split_kernel(const NsMat* tab, uint32_
     uint32_t r0, c0;
     prep_tile(m, blockIdx.x - m.prep0, r0, c0);
     const double inv = reinterpret_cast<const NsScaling*>(m.work + w.inv)->inv;
-    const uint32_t cc = threadIdx.x & 63u;
-#pragma unroll 4
-    for (uint32_t k = threadIdx.x >> 6; k < kNsPrep; k += 4) {
-        float x = 0.0f;
-        if (r0 + k < m.rows && c0 + cc < m.cols)
-            x = static_cast<float>(static_cast<double>(load_u<false>(m, r0 + k, c0 + cc)) * inv) * kNsScale;
-        tile[k][cc] = x;
-    }
+    const uint32_t cc = (threadIdx.x & 15u) * 4, rr = threadIdx.x >> 4;
+    f32x4 u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) u[k] = load_u4<false>(m, r0 + rr + 16 * k, c0 + cc);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            tile[rr + 16 * k][cc + e] = static_cast<float>(static_cast<double>(u[k][e]) * inv) * kNsScale;
     __syncthreads();
     const bool tall = (m.flags & kNsTall) != 0;
     char* xt = m.work + w.xt[0];
@@ -280,11 +365,11 @@ __global__ void __launch_bounds__(256) ns_split_kernel(const NsMat* tab, uint32_
             b[e] = tile[c + e][r];
         }
         if (tall) {
-            put_terms<kT, 2>(xt, r0 + r, m.mp, c0 + c, a);
+            put_terms<kT, kXTerms>(xt, r0 + r, m.mp, c0 + c, a);
             put_terms<kT, kGramTerms>(x, c0 + r, m.np, r0 + c, b);
         } else {
             put_terms<kT, kGramTerms>(x, r0 + r, m.np, c0 + c, a);
-            put_terms<kT, 2>(xt, c0 + r, m.mp, r0 + c, b);
+            put_terms<kT, kXTerms>(xt, c0 + r, m.mp, r0 + c, b);
         }
     }
 }
@@ -292,7 +377,7 @@ __global__ void __launch_bounds__(256) ns_split_kernel(const NsMat* tab, uint32_
 // ------------------------------------------------------ general path: products
 //
 // D[i][j] = sum over k of A[i][k] B[j][k], one tile of kT x kT per workgroup.
-// kT = 128: four waves, 64 x 64 each; kT = 256: eight waves, 128 x 64 each;
+// kT = 64 or 128: four waves, a quarter each; kT = 256: eight waves, 128 x 64 each;
 // in matrix-core tiles of 32 x 32.  A stage is one block of each operand (two
 // where both have one term); stages go round four buffers in LDS, loaded
 // straight to LDS three stages ahead of the one that is multiplied.
@@ -303,21 +388,24 @@ __global__ void __launch_bounds__(256) ns_split_kernel(const NsMat* tab, uint32_
 // the order of the parts, so the result does not depend on which that is.
 // Nobody waits for another workgroup.
 
-// Copy kBytes from g to lds, by all waves.
-template <int kWaves, uint32_t kBytes>
+// Copy kBytes from g to lds, by all waves (where there is less than a load for
+// each, several make the same one, so that all count alike).
+template <uint32_t kWaves, uint32_t kBytes>
 __device__ __forceinline__ void load_stage(const char* g, char* lds, uint32_t wave, uint32_t lane)
 {
+    constexpr uint32_t kAll = kBytes / 1024, kEach = kAll < kWaves ? 1 : kAll / kWaves;
+    static_assert(kAll * 1024 == kBytes && (kAll < kWaves ? kWaves % kAll == 0 : kAll % kWaves == 0), "whole loads");
 #pragma unroll
-    for (uint32_t q = 0; q < kBytes / 1024 / kWaves; ++q) {
-        const uint32_t at = (wave * (kBytes / 1024 / kWaves) + q) * 1024;
+    for (uint32_t q = 0; q < kEach; ++q) {
+        const uint32_t at = (wave * kEach + q) % kAll * 1024;
         __builtin_amdgcn_global_load_lds(
             reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(reinterpret_cast<uintptr_t>(g + at + lane * 16)),
             (__attribute__((address_space(3))) uint32_t*)(lds + at), 16, 0, 0);
     }
 }
 
-// Fragments of a stage: at LDS addresses a0 and a1 four or two of them
-// each, kA bytes apart, likewise two at b0 (and b1).  The reads and
+// Fragments of a stage: at LDS addresses a0 and a1 four, two or one of them
+// each, kA bytes apart, likewise two or one at b0 (and b1).  The reads and
 // the wait for them are one asm block, because the compiler would put a wait
 // for the loads of later stages (which go to other buffers) before reads of
 // LDS that it sees.
@@ -347,6 +435,26 @@ __device__ __forceinline__ void read_4_1(uint32_t a0, uint32_t a1, uint32_t b0, 
                  : "=&v"(fa[0][0]), "=&v"(fa[0][1]), "=&v"(fa[0][2]), "=&v"(fa[0][3]), "=&v"(fa[1][0]), "=&v"(fa[1][1]),
                    "=&v"(fa[1][2]), "=&v"(fa[1][3]), "=&v"(fb[0][0]), "=&v"(fb[0][1])
                  : "v"(a0), "v"(a1), "v"(b0), "n"(kA), "n"(kB)
+                 : "memory");
+}
+
+template <int kA, int kB>
+__device__ __forceinline__ void read_1_2(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1, f16x8 (&fa)[2][1], f16x8 (&fb)[2][1])
+{
+    asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %2, %6\n\tds_read_b128 %3, %7\n\tds_read_b128 %1, %5\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(fa[0][0]), "=&v"(fa[1][0]), "=&v"(fb[0][0]), "=&v"(fb[1][0])
+                 : "v"(a0), "v"(a1), "v"(b0), "v"(b1)
+                 : "memory");
+}
+
+template <int kA, int kB>
+__device__ __forceinline__ void read_1_1(uint32_t a0, uint32_t a1, uint32_t b0, f16x8 (&fa)[2][1], f16x8 (&fb)[1][1])
+{
+    asm volatile("ds_read_b128 %0, %3\n\tds_read_b128 %2, %5\n\tds_read_b128 %1, %4\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(fa[0][0]), "=&v"(fa[1][0]), "=&v"(fb[0][0])
+                 : "v"(a0), "v"(a1), "v"(b0)
                  : "memory");
 }
 
@@ -403,7 +511,8 @@ __device__ __forceinline__ void wait_loads_and_meet()
     meet();
 }
 
-enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
+// kApply leaves X^T in as many terms as it reads, kFewer in one.
+enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3, kFewer = 4 };
 
 struct ProductArgs {
     const NsMat* tab;
@@ -449,22 +558,27 @@ __device__ __forceinline__ void band_tile(uint32_t k, uint32_t tn, uint32_t tm, 
 }
 
 template <int kT, int kTermsA, int kTermsB, int kKind, int kGramTerms>
-__global__ void __launch_bounds__(kT == 128 ? 256 : 512, 2) ns_product_kernel(const ProductArgs args)
+__global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(const ProductArgs args)
 {
-    constexpr int kWaves = kT == 128 ? 4 : 8, kThreads = kWaves * 64;
-    constexpr int kWm = kT / 2, kWn = 64, kX = kWm / 32, kY = kWn / 32;   // a wave's part, in matrix-core tiles
+    constexpr int kWaves = kT == 256 ? 8 : 4, kThreads = kWaves * 64;
+    constexpr int kWm = kT / 2, kWn = kT == 256 ? 64 : kT / 2;            // a wave's part of the tile
+    constexpr int kX = kWm / 32, kY = kWn / 32;                           // in matrix-core tiles
     constexpr int kValues = (kTermsA == 1 && kTermsB == 1) ? 32 : 16;     // of the summed index per stage
     constexpr int kRowA = 32 * kTermsA, kRowB = 32 * kTermsB;             // bytes of a row in a block
     constexpr uint32_t kStageA = kT * 2 * kValues * kTermsA, kStageB = kT * 2 * kValues * kTermsB, kStage = kStageA + kStageB;
-    constexpr int kRing = 4, kLoads = kStage / 1024 / kWaves;             // loads of a wave per stage
-    constexpr uint32_t kPitch = kT + 1, kStrip = 128;                     // of the result tile in LDS
+    constexpr int kRing = 4;
+    constexpr auto loads_of = [](uint32_t bytes) { return bytes / 1024 < kWaves ? 1 : static_cast<int>(bytes / 1024 / kWaves); };
+    constexpr int kLoads = loads_of(kStageA) + loads_of(kStageB);         // of a wave per stage
+    constexpr uint32_t kPitch = kT + 1, kStrip = kT < 128 ? kT : 128;                     // of the result tile in LDS
     constexpr uint32_t kLds = kRing * kStage > kStrip * kPitch * 4 ? kRing * kStage : kStrip * kPitch * 4;
     __shared__ __attribute__((aligned(128))) char lds[kLds];
     __shared__ uint32_t last_part;
 
     const uint32_t mi = kKind <= kPoly ? (kKind == kGram ? find_mat<&NsMat::gram0>(args.tab, args.n, blockIdx.x)
                                                          : find_mat<&NsMat::poly0>(args.tab, args.n, blockIdx.x))
-                                       : find_mat<&NsMat::apply0>(args.tab, args.n, blockIdx.x);
+                                       : kTermsA == kTermsB && kGramTerms == 1
+                                             ? find_mat<&NsMat::apply_one0>(args.tab, args.n, blockIdx.x)
+                                             : find_mat<&NsMat::apply0>(args.tab, args.n, blockIdx.x);
     const NsMat m = load_mat(args.tab, mi);
     const NsWork w = ns_work(m.mp, m.np, kGramTerms);
     const char* a;
@@ -485,7 +599,7 @@ __global__ void __launch_bounds__(kT == 128 ? 256 : 512, 2) ns_product_kernel(co
         a = m.work + ((args.turn & 1u) ? w.xt[1] : w.xt[0]);
         b = m.work + w.p;
         depth = m.mp;
-        first = m.apply0;
+        first = kTermsA == kTermsB && kGramTerms == 1 ? m.apply_one0 : m.apply0;
         tiles = tm * tn;
     }
     const uint32_t stages = depth / kValues, parts = (stages + args.depth - 1) / args.depth;
@@ -506,7 +620,7 @@ __global__ void __launch_bounds__(kT == 128 ? 256 : 512, 2) ns_product_kernel(co
 
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)));
-    const uint32_t wi = (kT == 128 ? wave >> 1 : wave >> 2) * kWm, wj = (kT == 128 ? wave & 1u : wave & 3u) * kWn;
+    const uint32_t wi = (kT == 256 ? wave >> 2 : wave >> 1) * kWm, wj = (kT == 256 ? wave & 3u : wave & 1u) * kWn;
     f32x16 acc[kX][kY];
 #pragma unroll
     for (int x = 0; x < kX; ++x)
@@ -538,9 +652,11 @@ __global__ void __launch_bounds__(kT == 128 ? 256 : 512, 2) ns_product_kernel(co
         const uint32_t now = (s % kRing) * kStage;
         if constexpr (kNb == 2) {
             if constexpr (kX == 4) read_4_2<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, now + at_b1, fa, fb);
+            else if constexpr (kX == 1) read_1_2<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, now + at_b1, fa, fb);
             else read_2_2<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, now + at_b1, fa, fb);
         } else {
             if constexpr (kX == 4) read_4_1<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, fa, fb);
+            else if constexpr (kX == 1) read_1_1<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, fa, fb);
             else read_2_1<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, fa, fb);
         }
     };
@@ -576,7 +692,7 @@ __global__ void __launch_bounds__(kT == 128 ? 256 : 512, 2) ns_product_kernel(co
         load_a(s0 + s);
         load_b(s0 + s);
     }
-    if (kT == 128) {
+    if (kT < 256) {
         for (uint32_t s = s0; s < s1; ++s) {
             wait_loads_and_meet<2 * kLoads>();   // stage s is here, stage s - 1 has been read
             read(s);
@@ -689,15 +805,26 @@ __global__ void __launch_bounds__(kT == 128 ? 256 : 512, 2) ns_product_kernel(co
         if (kKind == kLast) {
             // D is X'^T: element (i, j) is X'(j, i); rows of the natural
             // matrix are i if tall, else j
-            if (m.flags & kNsTall) {
-                for (uint32_t v = threadIdx.x; v < kStrip * kT; v += kThreads) {
-                    const uint32_t r = v / kT, c = v % kT;
-                    if (is + r < m.rows && j0 + c < m.cols) put_result(m, is + r, j0 + c, tile[r * kPitch + c]);
+            const bool tall = (m.flags & kNsTall) != 0;
+            constexpr uint32_t kQuads = kStrip * kT / 4 / kThreads;   // per thread, four at a time
+            const uint32_t across = tall ? kT / 4 : kStrip / 4;
+            const uint32_t rr = tall ? is : j0, cr = tall ? j0 : is;
+            for (uint32_t q = 0; q < kQuads; q += 4) {
+                uint32_t r[4], c[4];
+                f32x4 old[4];
+#pragma unroll
+                for (uint32_t x = 0; x < 4; ++x) {
+                    const uint32_t v = threadIdx.x + (q + x) * kThreads;
+                    r[x] = v / across;
+                    c[x] = v % across * 4;
+                    old[x] = old_master4(m, rr + r[x], cr + c[x]);
                 }
-            } else {
-                for (uint32_t v = threadIdx.x; v < kStrip * kT; v += kThreads) {
-                    const uint32_t r = v / kStrip, c = v % kStrip;
-                    if (j0 + r < m.rows && is + c < m.cols) put_result(m, j0 + r, is + c, tile[c * kPitch + r]);
+#pragma unroll
+                for (uint32_t x = 0; x < 4; ++x) {
+                    f32x4 o;
+#pragma unroll
+                    for (uint32_t e = 0; e < 4; ++e) o[e] = tall ? tile[r[x] * kPitch + c[x] + e] : tile[(c[x] + e) * kPitch + r[x]];
+                    put_result4(m, rr + r[x], cr + c[x], o, old[x]);
                 }
             }
             continue;
@@ -705,7 +832,7 @@ __global__ void __launch_bounds__(kT == 128 ? 256 : 512, 2) ns_product_kernel(co
         char* out_rows;      // takes D
         char* out_cols;      // takes D transposed
         uint32_t ld_rows, ld_cols;
-        if (kKind == kApply) {
+        if (kKind > kPoly) {
             out_rows = m.work + ((args.turn & 1u) ? w.xt[0] : w.xt[1]);
             out_cols = m.work + w.x;
             ld_rows = m.mp;
@@ -732,10 +859,10 @@ __global__ void __launch_bounds__(kT == 128 ? 256 : 512, 2) ns_product_kernel(co
 #pragma unroll
                 for (int e = 0; e < 8; ++e) d[e] = tile[r * kPitch + c + e];
                 if (kKind == kPoly) polynomial(is + r, j0 + c, d);
-                if (kKind == kApply) put_terms<kT, 2>(out_rows, is + r, ld_rows, j0 + c, d);
+                if (kKind > kPoly) put_terms<kT, kKind == kFewer ? 1 : kTermsA>(out_rows, is + r, ld_rows, j0 + c, d);
                 else put_terms<kT, kGramTerms>(out_rows, is + r, ld_rows, j0 + c, d);
             }
-            if (kKind == kApply || ti != tj) {
+            if (kKind > kPoly || ti != tj) {
                 const uint32_t c = (v & 1u) * 8 + v / (kT * 2) * 16, r = (v >> 1) % kT;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) d[e] = tile[(c + e) * kPitch + r];
@@ -757,60 +884,85 @@ __global__ void __launch_bounds__(kT == 128 ? 256 : 512, 2) ns_product_kernel(co
 // over five steps; in FP64 it ends near 1e-11.  |u|_F^2 is the trace of the
 // unscaled S.  Bound: two reads of u and launch latency.
 
+constexpr uint32_t kSmallPitch = kNsSmallChunk + 1;
+
+// Four columns of the natural matrix that thread number v stages: quads of a
+// row after another.  Returns the row and column; (p, x) is the first
+// element's place in u (smaller side, long side) and `step` the way to the
+// next one.
 template <int kK>
-__device__ __forceinline__ void small_place(const NsMat& m, uint32_t p, uint32_t l, uint32_t& r, uint32_t& c)
+__device__ __forceinline__ void small_quad(bool tall, uint32_t v, uint32_t l0, uint32_t& r, uint32_t& c, uint32_t& at, uint32_t& step)
 {
-    const bool tall = (m.flags & kNsTall) != 0;
-    r = tall ? l : p;
-    c = tall ? p : l;
+    const uint32_t across = tall ? kK / 4 : kNsSmallChunk / 4, i = v / across, j = v % across * 4;
+    r = tall ? l0 + i : i;
+    c = tall ? j : l0 + j;
+    at = tall ? j * kSmallPitch + i : i * kSmallPitch + j;
+    step = tall ? kSmallPitch : 1;
 }
 
-// Stage u of long-side elements [l0, l0 + count) into u[p][l - l0].
+// Stage u of long-side elements [l0, l0 + kNsSmallChunk) as u[p][x], zeros
+// outside the matrix.
 template <int kK, bool kFirst>
-__device__ __forceinline__ void stage_u(const NsMat& m, uint32_t k, uint32_t l0, uint32_t count, float (&u)[kK][kNsSmallChunk + 1])
+__device__ __forceinline__ void stage_u(const NsMat& m, uint32_t l0, float* u)
 {
     const bool tall = (m.flags & kNsTall) != 0;
-    for (uint32_t v = threadIdx.x; v < k * count; v += 256) {
-        // natural order: consecutive v are consecutive columns
-        const uint32_t p = tall ? v % k : v / count, l = tall ? v / k : v % count;
+    constexpr int kQuads = kK / 4;   // per thread
+    f32x4 q[kQuads];
+    uint32_t at[kQuads], step;
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) {
         uint32_t r, c;
-        small_place<kK>(m, p, l0 + l, r, c);
-        u[p][l] = load_u<kFirst>(m, r, c);
+        small_quad<kK>(tall, threadIdx.x + k * 256, l0, r, c, at[k], step);
+        q[k] = load_u4<kFirst>(m, r, c);
     }
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[at[k] + e * step] = q[k][e];
 }
 
 template <int kK>
 __global__ void __launch_bounds__(256) ns_small_gram_kernel(const NsMat* tab, uint32_t n)
 {
-    __shared__ float u[kK][kNsSmallChunk + 1];
+    __shared__ float u[kK * kSmallPitch];
     __shared__ double part[256];
     const NsMat m = load_mat(tab, find_mat<&NsMat::prep0>(tab, n, blockIdx.x));
-    const uint32_t chunk = blockIdx.x - m.prep0;
-    const uint32_t k = m.rows < m.cols ? m.rows : m.cols, l = m.rows < m.cols ? m.cols : m.rows;
-    const uint32_t l0 = chunk * kNsSmallChunk, count = l - l0 < kNsSmallChunk ? l - l0 : kNsSmallChunk;
-    stage_u<kK, true>(m, k, l0, count, u);
+    const uint32_t chunk = blockIdx.x - m.prep0, k = m.rows < m.cols ? m.rows : m.cols;
+    stage_u<kK, true>(m, chunk * kNsSmallChunk, u);
     __syncthreads();
     double* out = reinterpret_cast<double*>(m.work) + static_cast<uint64_t>(chunk) * k * k;
-    constexpr uint32_t kSlots = kK * kK;
-    if (kSlots >= 256) {
-        for (uint32_t s = threadIdx.x; s < kSlots; s += 256) {
-            const uint32_t p = s / kK, q = s % kK;
-            if (p >= k || q >= k) continue;
-            double sum = 0.0;
-            for (uint32_t x = 0; x < count; ++x) sum = fma(static_cast<double>(u[p][x]), static_cast<double>(u[q][x]), sum);
-            out[p * k + q] = sum;
+    if constexpr (kK == 32) {
+        // a thread takes (p, q), (p + 16, q), (p, q + 16) and (p + 16, q + 16)
+        const uint32_t p = threadIdx.x >> 4, q = threadIdx.x & 15u;
+        double s00 = 0.0, s01 = 0.0, s10 = 0.0, s11 = 0.0;
+#pragma unroll 4
+        for (uint32_t x = 0; x < kNsSmallChunk; ++x) {
+            const double a0 = u[p * kSmallPitch + x], a1 = u[(p + 16) * kSmallPitch + x];
+            const double b0 = u[q * kSmallPitch + x], b1 = u[(q + 16) * kSmallPitch + x];
+            s00 = fma(a0, b0, s00);
+            s01 = fma(a0, b1, s01);
+            s10 = fma(a1, b0, s10);
+            s11 = fma(a1, b1, s11);
         }
+        if (p < k && q < k) out[p * k + q] = s00;
+        if (p < k && q + 16 < k) out[p * k + q + 16] = s01;
+        if (p + 16 < k && q < k) out[(p + 16) * k + q] = s10;
+        if (p + 16 < k && q + 16 < k) out[(p + 16) * k + q + 16] = s11;
     } else {
-        // several threads per (p, q), each over its own part of the chunk
-        constexpr uint32_t kParts = 256 / kSlots;
+        // 256 / (kK * kK) threads per (p, q), each over its own part of the chunk
+        constexpr uint32_t kSlots = kK * kK, kParts = 256 / kSlots, kLen = kNsSmallChunk / kParts;
         const uint32_t s = threadIdx.x % kSlots, g = threadIdx.x / kSlots, p = s / kK, q = s % kK;
-        double sum = 0.0;
-        if (p < k && q < k)
-            for (uint32_t x = g * (kNsSmallChunk / kParts); x < (g + 1) * (kNsSmallChunk / kParts) && x < count; ++x)
-                sum = fma(static_cast<double>(u[p][x]), static_cast<double>(u[q][x]), sum);
+        double sum0 = 0.0, sum1 = 0.0;
+#pragma unroll 8
+        for (uint32_t x = g * kLen; x < (g + 1) * kLen; x += 2) {
+            sum0 = fma(static_cast<double>(u[p * kSmallPitch + x]), static_cast<double>(u[q * kSmallPitch + x]), sum0);
+            sum1 = fma(static_cast<double>(u[p * kSmallPitch + x + 1]), static_cast<double>(u[q * kSmallPitch + x + 1]), sum1);
+        }
+        double sum = sum0 + sum1;
         part[threadIdx.x] = sum;
         __syncthreads();
         if (g == 0 && p < k && q < k) {
+#pragma unroll
             for (uint32_t x = 1; x < kParts; ++x) sum += part[x * kSlots + s];
             out[p * k + q] = sum;
         }
@@ -824,82 +976,152 @@ struct SmallArgs {
     double coef[3 * kNsMaxSteps];
 };
 
-// One workgroup of kK * kK threads per matrix, one element each.
-template <int kK>
-__global__ void __launch_bounds__(kK * kK) ns_small_iterate_kernel(const SmallArgs args)
+// One workgroup per matrix, kB x kB elements of every k x k matrix per thread.
+template <int kK, int kB>
+__global__ void __launch_bounds__(kK * kK / (kB * kB)) ns_small_iterate_kernel(const SmallArgs args)
 {
+    constexpr int kSide = kK / kB;
     __shared__ double s[kK][kK + 1], t[kK][kK + 1], p[kK][kK + 1], q[kK][kK + 1];
     const NsMat m = load_mat(args.tab, blockIdx.x);
     const uint32_t k = m.rows < m.cols ? m.rows : m.cols, l = m.rows < m.cols ? m.cols : m.rows;
     const uint32_t chunks = (l + kNsSmallChunk - 1) / kNsSmallChunk;
-    const uint32_t i = threadIdx.x / kK, j = threadIdx.x % kK;
-    const bool in = i < k && j < k;
+    const uint32_t i = threadIdx.x / kSide, j = threadIdx.x % kSide;   // and i + kSide, ...
     const double* part = reinterpret_cast<const double*>(m.work);
-    double sum = 0.0;
-    if (in)
-        for (uint32_t c = 0; c < chunks; ++c) sum += part[static_cast<uint64_t>(c) * k * k + i * k + j];
-    s[i][j] = sum;
+    double v[kB][kB];
+#pragma unroll
+    for (int x = 0; x < kB; ++x)
+#pragma unroll
+        for (int y = 0; y < kB; ++y) {
+            const uint32_t ii = i + x * kSide, jj = j + y * kSide;
+            double sum = 0.0;
+            if (ii < k && jj < k) {
+                const double* from = part + ii * k + jj;
+#pragma unroll 8
+                for (uint32_t c = 0; c < chunks; ++c) sum += from[static_cast<uint64_t>(c) * k * k];
+            }
+            v[x][y] = sum;
+            s[ii][jj] = sum;
+        }
     __syncthreads();
     double trace = 0.0;
-    for (uint32_t x = 0; x < k; ++x) trace += s[x][x];
+#pragma unroll
+    for (int x = 0; x < kK; ++x) trace += s[x][x];   // zeros from k on
     const double inv = 1.0 / (sqrt(trace) + args.eps);
     __syncthreads();
-    s[i][j] = sum * inv * inv;
-    q[i][j] = i == j ? inv : 0.0;   // Q_0 carries the scaling of u to X_0
-    __syncthreads();
-    auto product = [&](const double (&x)[kK][kK + 1], const double (&y)[kK][kK + 1]) {
-        double v = 0.0;
-        for (uint32_t e = 0; e < k; ++e) v = fma(x[i][e], y[e][j], v);
-        return v;
+    auto put = [&](double (&to)[kK][kK + 1], const double (&from)[kB][kB]) {
+#pragma unroll
+        for (int x = 0; x < kB; ++x)
+#pragma unroll
+            for (int y = 0; y < kB; ++y) to[i + x * kSide][j + y * kSide] = from[x][y];
     };
+    auto product = [&](const double (&a)[kK][kK + 1], const double (&b)[kK][kK + 1], double (&out)[kB][kB]) {
+#pragma unroll
+        for (int x = 0; x < kB; ++x)
+#pragma unroll
+            for (int y = 0; y < kB; ++y) out[x][y] = 0.0;
+#pragma unroll 8
+        for (int e = 0; e < kK; ++e) {
+            double ax[kB], by[kB];
+#pragma unroll
+            for (int x = 0; x < kB; ++x) {
+                ax[x] = a[i + x * kSide][e];
+                by[x] = b[e][j + x * kSide];
+            }
+#pragma unroll
+            for (int x = 0; x < kB; ++x)
+#pragma unroll
+                for (int y = 0; y < kB; ++y) out[x][y] = fma(ax[x], by[y], out[x][y]);
+        }
+    };
+    double w[kB][kB];
+#pragma unroll
+    for (int x = 0; x < kB; ++x)
+#pragma unroll
+        for (int y = 0; y < kB; ++y) {
+            v[x][y] = v[x][y] * inv * inv;
+            w[x][y] = i + x * kSide == j + y * kSide ? inv : 0.0;   // Q_0 carries the scaling of u to X_0
+        }
+    put(s, v);
+    put(q, w);
+    __syncthreads();
     for (uint32_t n = 0; n < args.steps; ++n) {
         const double a = args.coef[3 * n], b = args.coef[3 * n + 1], c = args.coef[3 * n + 2];
-        const double s2 = product(s, s);
-        p[i][j] = (i == j ? a : 0.0) + b * s[i][j] + c * s2;
+        product(s, s, w);
+#pragma unroll
+        for (int x = 0; x < kB; ++x)
+#pragma unroll
+            for (int y = 0; y < kB; ++y)
+                w[x][y] = (i + x * kSide == j + y * kSide ? a : 0.0) + b * s[i + x * kSide][j + y * kSide] + c * w[x][y];
+        put(p, w);
         __syncthreads();
-        const double qn = product(p, q);
-        t[i][j] = product(p, s);
+        product(p, s, w);
+        put(t, w);
+        product(p, q, w);
         __syncthreads();
-        q[i][j] = qn;
-        s[i][j] = product(t, p);
+        put(q, w);
+        product(t, p, w);
+        put(s, w);
         __syncthreads();
     }
-    if (in) reinterpret_cast<double*>(m.work)[static_cast<uint64_t>(chunks) * k * k + i * k + j] = q[i][j];
+    double* out = reinterpret_cast<double*>(m.work) + static_cast<uint64_t>(chunks) * k * k;
+#pragma unroll
+    for (int x = 0; x < kB; ++x)
+#pragma unroll
+        for (int y = 0; y < kB; ++y) {
+            const uint32_t ii = i + x * kSide, jj = j + y * kSide;
+            if (ii < k && jj < k) out[ii * k + jj] = q[ii][jj];
+        }
 }
 
 template <int kK>
 __global__ void __launch_bounds__(256) ns_small_apply_kernel(const NsMat* tab, uint32_t n)
 {
-    __shared__ float u[kK][kNsSmallChunk + 1];
+    __shared__ float u[kK * kSmallPitch];
     __shared__ double q[kK * kK];
     const NsMat m = load_mat(tab, find_mat<&NsMat::prep0>(tab, n, blockIdx.x));
-    const uint32_t chunk = blockIdx.x - m.prep0;
+    const uint32_t l0 = (blockIdx.x - m.prep0) * kNsSmallChunk;
     const uint32_t k = m.rows < m.cols ? m.rows : m.cols, l = m.rows < m.cols ? m.cols : m.rows;
-    const uint32_t l0 = chunk * kNsSmallChunk, count = l - l0 < kNsSmallChunk ? l - l0 : kNsSmallChunk;
     const uint32_t chunks = (l + kNsSmallChunk - 1) / kNsSmallChunk;
-    stage_u<kK, false>(m, k, l0, count, u);
+    const bool tall = (m.flags & kNsTall) != 0;
+    constexpr int kQuads = kK / 4;
+    f32x4 old[kQuads];
+#pragma unroll
+    for (int x = 0; x < kQuads; ++x) {
+        uint32_t r, c, at, step;
+        small_quad<kK>(tall, threadIdx.x + x * 256, l0, r, c, at, step);
+        old[x] = old_master4(m, r, c);
+    }
+    stage_u<kK, false>(m, l0, u);
     const double* src = reinterpret_cast<const double*>(m.work) + static_cast<uint64_t>(chunks) * k * k;
-    for (uint32_t v = threadIdx.x; v < k * k; v += 256) q[v] = src[v];
-    __syncthreads();
-    if (threadIdx.x < count) {
-        float col[kK];
-#pragma unroll
-        for (int e = 0; e < kK; ++e) col[e] = e < static_cast<int>(k) ? u[e][threadIdx.x] : 0.0f;
-        for (uint32_t p = 0; p < k; ++p) {
-            double v = 0.0;
-#pragma unroll
-            for (int e = 0; e < kK; ++e)
-                if (e < static_cast<int>(k)) v = fma(q[p * k + e], static_cast<double>(col[e]), v);
-            u[p][threadIdx.x] = static_cast<float>(v);
-        }
+    for (uint32_t v = threadIdx.x; v < kK * kK; v += 256) {
+        const uint32_t i = v / kK, j = v % kK;
+        q[v] = i < k && j < k ? src[i * k + j] : 0.0;
     }
     __syncthreads();
-    const bool tall = (m.flags & kNsTall) != 0;
-    for (uint32_t v = threadIdx.x; v < k * count; v += 256) {
-        const uint32_t p = tall ? v % k : v / count, x = tall ? v / k : v % count;
-        uint32_t r, c;
-        small_place<kK>(m, p, l0 + x, r, c);
-        put_result(m, r, c, u[p][x]);
+    // one column of u per thread, four rows of the result at a time
+    float col[kK];
+#pragma unroll
+    for (int e = 0; e < kK; ++e) col[e] = u[e * kSmallPitch + threadIdx.x];
+    for (uint32_t p = 0; p < k; p += 4) {
+        double v[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+        for (int e = 0; e < kK; ++e) {
+            const double x = col[e];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) v[y] = fma(q[(p + y) * kK + e], x, v[y]);
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) u[(p + y) * kSmallPitch + threadIdx.x] = static_cast<float>(v[y]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kQuads; ++x) {
+        uint32_t r, c, at, step;
+        small_quad<kK>(tall, threadIdx.x + x * 256, l0, r, c, at, step);
+        f32x4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = u[at + e * step];
+        put_result4(m, r, c, o, old[x]);
     }
 }
 
@@ -912,7 +1134,8 @@ hipError_t launch_small(const NsCall& c, const NsMat* tab, uint32_t n, uint32_t 
     args.eps = c.eps;
     for (uint32_t k = 0; k < 3 * c.steps; ++k) args.coef[k] = c.coef[k];
     hipLaunchKernelGGL(ns_small_gram_kernel<kK>, dim3(chunks), dim3(256), 0, s, tab, n);
-    hipLaunchKernelGGL(ns_small_iterate_kernel<kK>, dim3(n), dim3(kK * kK), 0, s, args);
+    constexpr int kB = kK == 32 ? 2 : 1;
+    hipLaunchKernelGGL((ns_small_iterate_kernel<kK, kB>), dim3(n), dim3(kK * kK / (kB * kB)), 0, s, args);
     hipLaunchKernelGGL(ns_small_apply_kernel<kK>, dim3(chunks), dim3(256), 0, s, tab, n);
     return hipGetLastError();
 }
@@ -923,8 +1146,13 @@ hipError_t launch_big(const NsCall& c, const NsMat* tab, hipStream_t s)
     const uint32_t n = c.nbig;
     hipLaunchKernelGGL(ns_norm_kernel, dim3(c.prep_tiles), dim3(256), 0, s, tab, n, c.gram_terms, c.counters, c.ncounters);
     hipLaunchKernelGGL(ns_scale_kernel, dim3(n), dim3(1024), 0, s, tab, c.gram_terms, c.eps);
-    hipLaunchKernelGGL((ns_split_kernel<kT, kGramTerms>), dim3(c.prep_tiles), dim3(256), 0, s, tab, n);
-    const dim3 threads(kT == 128 ? 256 : 512);
+    // X^T keeps its l terms for all but the last two steps (or for all, in full
+    // precision): what a later step does not magnify is below the rounding
+    // of S and P anyway
+    const uint32_t twice = kGramTerms == 2 ? c.steps : c.steps > 2 ? c.steps - 2 : 0;
+    if (twice > 0) hipLaunchKernelGGL((ns_split_kernel<kT, kGramTerms, 2>), dim3(c.prep_tiles), dim3(256), 0, s, tab, n);
+    else hipLaunchKernelGGL((ns_split_kernel<kT, kGramTerms, 1>), dim3(c.prep_tiles), dim3(256), 0, s, tab, n);
+    const dim3 threads(kT == 256 ? 512 : 256);
     int lowered = 0;
     for (uint32_t k = 0; k < c.steps; ++k) {
         ProductArgs args{};
@@ -943,11 +1171,16 @@ hipError_t launch_big(const NsCall& c, const NsMat* tab, hipStream_t s)
         hipLaunchKernelGGL((ns_product_kernel<kT, kGramTerms, kGramTerms, kGram, kGramTerms>), dim3(c.gram.units), threads, 0, s, args);
         args.depth = c.poly.depth;
         hipLaunchKernelGGL((ns_product_kernel<kT, kGramTerms, kGramTerms, kPoly, kGramTerms>), dim3(c.poly.units), threads, 0, s, args);
-        args.depth = c.apply.depth;
-        if (k + 1 < c.steps)
-            hipLaunchKernelGGL((ns_product_kernel<kT, 2, kGramTerms, kApply, kGramTerms>), dim3(c.apply.units), threads, 0, s, args);
-        else
-            hipLaunchKernelGGL((ns_product_kernel<kT, 2, kGramTerms, kLast, kGramTerms>), dim3(c.apply.units), threads, 0, s, args);
+        // (a stage of one-term operands holds twice the values)
+        const dim3 apply(c.apply.units), apply_one(c.apply_one.units);
+        const bool last = k + 1 == c.steps;
+        args.depth = k < twice ? c.apply.depth : c.apply_one.depth;
+        if (k < twice && last) hipLaunchKernelGGL((ns_product_kernel<kT, 2, kGramTerms, kLast, kGramTerms>), apply, threads, 0, s, args);
+        else if (k + 1 < twice || kGramTerms == 2)
+            hipLaunchKernelGGL((ns_product_kernel<kT, 2, kGramTerms, kApply, kGramTerms>), apply, threads, 0, s, args);
+        else if (k < twice) hipLaunchKernelGGL((ns_product_kernel<kT, 2, 1, kFewer, 1>), apply, threads, 0, s, args);
+        else if (last) hipLaunchKernelGGL((ns_product_kernel<kT, 1, 1, kLast, 1>), apply_one, threads, 0, s, args);
+        else hipLaunchKernelGGL((ns_product_kernel<kT, 1, 1, kApply, 1>), apply_one, threads, 0, s, args);
     }
     return hipGetLastError();
 }
@@ -960,12 +1193,9 @@ int ns_launch(const NsCall& c, NsMat* device_table, void* stream)
     (void)hipGetLastError();   // an error left by other work is not this call's
     uint32_t total = c.nbig;
     for (int k = 0; k < kNsClasses; ++k) total += c.nsmall[k];
-    for (uint32_t k = 0; k < total; k += kWriteMats) {
-        NsTablePart part{};
-        part.dst = device_table + k;
-        part.count = total - k < kWriteMats ? total - k : kWriteMats;
-        for (uint32_t j = 0; j < part.count; ++j) part.src[j] = c.table[k + j];
-        hipLaunchKernelGGL(ns_table_kernel, dim3(1), dim3(64), 0, s, part);
+    for (uint32_t k = 0; k < total; k += kWriteMany) {
+        if (total - k <= kWriteFew) write_table<kWriteFew>(device_table + k, c.table + k, total - k, s);
+        else write_table<kWriteMany>(device_table + k, c.table + k, total - k < kWriteMany ? total - k : kWriteMany, s);
     }
     hipError_t err = hipGetLastError();
     const NsMat* tab = device_table;
@@ -978,6 +1208,7 @@ int ns_launch(const NsCall& c, NsMat* device_table, void* stream)
     }
     if (err == hipSuccess && c.nbig > 0) {
         if (c.tile == 256) err = c.gram_terms == 1 ? launch_big<256, 1>(c, tab, s) : launch_big<256, 2>(c, tab, s);
+        else if (c.tile == 64) err = c.gram_terms == 1 ? launch_big<64, 1>(c, tab, s) : launch_big<64, 2>(c, tab, s);
         else err = c.gram_terms == 1 ? launch_big<128, 1>(c, tab, s) : launch_big<128, 2>(c, tab, s);
     }
     return err;
