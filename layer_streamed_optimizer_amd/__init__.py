@@ -45,11 +45,19 @@ __all__ = ["BlockTable", "adam_step", "adam_step_noalloc", "adam_step_norms", "l
            "shadow_state", "shadow_commit", "stream_handle", "tiled_state_bytes", "tiled_pack", "tiled_unpack"]
 
 
+_raw_stream = None
+
+
 def stream_handle(stream=None) -> int:
     """hipStream_t of a torch stream, an int handle, or torch's current stream."""
     if stream is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            # the handle alone costs a tenth of making a Stream object
+            raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+            _raw_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+        return int(_raw_stream())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)

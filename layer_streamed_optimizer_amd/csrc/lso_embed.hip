@@ -14,6 +14,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 #include <vector>
 
 #include "lso_bf16.h"
@@ -31,8 +32,19 @@ constexpr uint32_t kMaxDigitBits = 10;
 constexpr uint32_t kMaxBins = 1u << kMaxDigitBits;
 constexpr uint32_t kSortThreads = 256;
 constexpr uint32_t kMaxSortGroups = 64;  // every group reads all groups' counts
-constexpr uint32_t kMinSortTile = 2048;
+constexpr uint32_t kMinSortTile = 512;
+constexpr uint32_t kRankSort = 4096;     // up to so many tokens are sorted by counting
 constexpr uint64_t kMaxGroups = (1ull << 24) - 1;   // workgroups of a launch: 256 lanes each, under 2^32 in all
+
+// Where the rows of a call exceed the eight XCDs' L2s (4 MB each), a lookup's
+// rows are stored past them, and a gradient's rows are read past them.
+// Measured: 16384 tokens of width 2048 looked up in 16.9 against 18.5 us; the
+// gradient of 32768 tokens of width 4096 in 151 against 177 us, of 131072 of
+// width 8192 in 815 against 860 us.  It costs where the rows are small (the
+// gradient of 257 tokens of width 2048 46 against 34 us), on the table's rows
+// that a lookup reads and tokens share (29.6 us), and on the gradient's table
+// (163 us).
+constexpr uint64_t kL2Bytes = 32ull << 20;
 
 // The sorted positions do not change while a gradient kernel runs, and a
 // wave reads the same one in every lane: scalar loads.
@@ -51,8 +63,9 @@ __device__ __forceinline__ uint32_t token_key(const Tokens& t, uint32_t i)
     return v >= 0 && v < static_cast<int64_t>(t.vocab) ? static_cast<uint32_t>(v) : t.vocab;
 }
 
-// V consecutive values of a row.
-template <int V, bool kF32>
+// V consecutive values of a row.  kOnce: they are not read again soon, and
+// pass the caches (non-temporal).
+template <int V, bool kF32, bool kOnce>
 __device__ __forceinline__ void load_values(const void* base, uint64_t i, float (&v)[V])
 {
     if (kF32) {
@@ -62,7 +75,8 @@ __device__ __forceinline__ void load_values(const void* base, uint64_t i, float 
         } else {
 #pragma unroll
             for (int e = 0; e < V; e += 4) {
-                const f32x4 x = *reinterpret_cast<const f32x4*>(p + e);
+                const f32x4* q = reinterpret_cast<const f32x4*>(p + e);
+                const f32x4 x = kOnce ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
                 for (int k = 0; k < 4 && e + k < V; ++k) v[e + k] = x[k];
             }
@@ -72,7 +86,8 @@ __device__ __forceinline__ void load_values(const void* base, uint64_t i, float 
         if (V == 1) {
             v[0] = bf16_widen(*p);
         } else {
-            const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+            const u32x4* q = reinterpret_cast<const u32x4*>(p);
+            const u32x4 x = kOnce ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
             for (int k = 0; k < 4 && 2 * k + 1 < V; ++k) {
                 v[2 * k] = bf16_widen(x[k] & 0xFFFFu);
@@ -82,7 +97,7 @@ __device__ __forceinline__ void load_values(const void* base, uint64_t i, float 
     }
 }
 
-template <int V, bool kF32>
+template <int V, bool kF32, bool kOnce>
 __device__ __forceinline__ void store_values(void* base, uint64_t i, const float (&v)[V])
 {
     if (kF32) {
@@ -91,7 +106,11 @@ __device__ __forceinline__ void store_values(void* base, uint64_t i, const float
             *p = v[0];
         } else {
 #pragma unroll
-            for (int e = 0; e + 3 < V; e += 4) *reinterpret_cast<f32x4*>(p + e) = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
+            for (int e = 0; e + 3 < V; e += 4) {
+                const f32x4 x = {v[e], v[e + 1], v[e + 2], v[e + 3]};
+                if (kOnce) __builtin_nontemporal_store(x, reinterpret_cast<f32x4*>(p + e));
+                else *reinterpret_cast<f32x4*>(p + e) = x;
+            }
         }
     } else {
         uint16_t* p = static_cast<uint16_t*>(base) + i;
@@ -101,7 +120,8 @@ __device__ __forceinline__ void store_values(void* base, uint64_t i, const float
             u32x4 x;
 #pragma unroll
             for (int k = 0; k < 4 && 2 * k + 1 < V; ++k) x[k] = bf16_rne(v[2 * k]) | (bf16_rne(v[2 * k + 1]) << 16);
-            *reinterpret_cast<u32x4*>(p) = x;
+            if (kOnce) __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(p));
+            else *reinterpret_cast<u32x4*>(p) = x;
         }
     }
 }
@@ -119,7 +139,7 @@ struct LookupArgs {
     float scale;
 };
 
-template <int V, bool kTableF32, bool kRowsF32>
+template <int V, bool kTableF32, bool kRowsF32, bool kOnce>
 __global__ void __launch_bounds__(256) embed_lookup_kernel(const LookupArgs a)
 {
     const uint64_t job = static_cast<uint64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
@@ -133,21 +153,21 @@ __global__ void __launch_bounds__(256) embed_lookup_kernel(const LookupArgs a)
         if (c >= a.width) break;
         float v[V];
         if (key < a.tokens.vocab) {
-            load_values<V, kTableF32>(a.table, key * a.ld_table + c, v);
+            load_values<V, kTableF32, false>(a.table, key * a.ld_table + c, v);
 #pragma unroll
             for (int e = 0; e < V; ++e) v[e] *= a.scale;
         } else {
 #pragma unroll
             for (int e = 0; e < V; ++e) v[e] = 0.0f;
         }
-        store_values<V, kRowsF32>(a.rows, i * a.ld_rows + c, v);
+        store_values<V, kRowsF32, kOnce>(a.rows, i * a.ld_rows + c, v);
     }
 }
 
 // -------------------------------------------------------------------- sort
 //
 // Least significant digit first, at most kMaxDigitBits bits a pass.  Each
-// group of threads owns a consecutive part of the input; counts[bin][group]
+// group of threads owns a consecutive part of the input; counts[group][bin]
 // says how many of its keys fall into each bin.
 
 struct SortArgs {
@@ -175,7 +195,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs
         if (begin + k < a.tokens.n)
             atomicAdd(&count[(sort_key(a, static_cast<uint32_t>(begin + k)) >> a.shift) & (bins - 1)], 1u);
     __syncthreads();
-    for (uint32_t b = threadIdx.x; b < bins; b += kSortThreads) a.counts[b * a.groups + blockIdx.x] = count[b];
+    for (uint32_t b = threadIdx.x; b < bins; b += kSortThreads) a.counts[blockIdx.x * bins + b] = count[b];
 }
 
 __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const SortArgs a)
@@ -189,12 +209,14 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const SortAr
     for (uint32_t b0 = 0; b0 < bins; b0 += kSortThreads) {
         const uint32_t b = b0 + threadIdx.x;
         uint32_t total = 0, before = 0;
-        if (b < bins)
+        if (b < bins) {
+#pragma unroll 8
             for (uint32_t g = 0; g < a.groups; ++g) {
-                const uint32_t c = a.counts[b * a.groups + g];
+                const uint32_t c = a.counts[g * bins + b];
                 if (g < blockIdx.x) before += c;
                 total += c;
             }
+        }
         uint32_t scan = total;   // inclusive over the wave
 #pragma unroll
         for (uint32_t off = 1; off < 64; off <<= 1) {
@@ -244,6 +266,51 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const SortAr
     }
 }
 
+// Up to kRankSort tokens, in one launch: an element's place is the number of
+// smaller keys and of equal keys before it.  A workgroup places 64 elements,
+// sixteen threads count for each.
+struct RankArgs {
+    Tokens tokens;
+    uint32_t* keys_out;
+    uint32_t* pos_out;
+};
+
+__global__ void __launch_bounds__(1024) sort_by_rank_kernel(const RankArgs a)
+{
+    __shared__ __attribute__((aligned(16))) uint32_t keys[kRankSort];
+    __shared__ uint32_t count[16][64];
+    const uint32_t n = a.tokens.n, padded = (n + 63) / 64 * 64;
+    for (uint32_t i = threadIdx.x; i < padded; i += 1024) keys[i] = i < n ? token_key(a.tokens, i) : 0xFFFFFFFFu;
+    __syncthreads();
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, i = blockIdx.x * 64 + lane, key = keys[i];
+    // wave w counts in blocks w, w + 16, ... of 64 keys: in blocks before the
+    // element's an equal key counts, in later ones it does not
+    uint32_t smaller = 0;
+    for (uint32_t b = wave; b < padded / 64; b += 16) {
+        const uint32_t* block = keys + b * 64;
+        if (b == blockIdx.x) {
+            for (uint32_t j = 0; j < 64; ++j) smaller += (block[j] < key || (block[j] == key && j < lane)) ? 1u : 0u;
+            continue;
+        }
+        const uint32_t limit = b < blockIdx.x ? key + 1 : key;   // a key is at most 2^31 (but for the padding's, unused)
+#pragma unroll 4
+        for (uint32_t j = 0; j < 64; j += 4) {
+            const u32x4 k4 = *reinterpret_cast<const u32x4*>(block + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) smaller += k4[e] < limit ? 1u : 0u;
+        }
+    }
+    count[wave][lane] = smaller;
+    __syncthreads();
+    if (wave == 0 && i < n) {
+        uint32_t to = 0;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) to += count[w][lane];
+        a.keys_out[to] = key;
+        a.pos_out[to] = i;
+    }
+}
+
 // ---------------------------------------------------------------- gradient
 
 struct GradArgs {
@@ -280,7 +347,7 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return static_cast<uin
 
 // Sum of the rows at sorted positions [first, first + count), at columns c
 // and on; first and count are the same in every lane.
-template <int V, bool kRowsF32>
+template <int V, bool kRowsF32, bool kOnce>
 __device__ __forceinline__ void sum_rows(const GradArgs& a, uint32_t first, uint32_t count, uint32_t c, float (&sum)[V])
 {
     const LSO_CONST uint32_t* pos = reinterpret_cast<const LSO_CONST uint32_t*>(reinterpret_cast<uintptr_t>(a.pos + first));
@@ -290,7 +357,7 @@ __device__ __forceinline__ void sum_rows(const GradArgs& a, uint32_t first, uint
     for (; k + 4 <= count; k += 4) {
         float v[4][V];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) load_values<V, kRowsF32>(a.rows, pos[k + x] * a.ld_rows + c, v[x]);
+        for (int x = 0; x < 4; ++x) load_values<V, kRowsF32, kOnce>(a.rows, pos[k + x] * a.ld_rows + c, v[x]);
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -298,7 +365,7 @@ __device__ __forceinline__ void sum_rows(const GradArgs& a, uint32_t first, uint
     }
     for (; k < count; ++k) {
         float v[V];
-        load_values<V, kRowsF32>(a.rows, pos[k] * a.ld_rows + c, v);
+        load_values<V, kRowsF32, kOnce>(a.rows, pos[k] * a.ld_rows + c, v);
 #pragma unroll
         for (int e = 0; e < V; ++e) sum[e] += v[e];
     }
@@ -312,29 +379,11 @@ __device__ __forceinline__ void put_gradient(const GradArgs& a, uint32_t v, uint
     for (int e = 0; e < V; ++e) sum[e] *= a.scale;
     if (a.add) {
         float old[V];
-        load_values<V, kTableF32>(a.table, i, old);
+        load_values<V, kTableF32, false>(a.table, i, old);
 #pragma unroll
         for (int e = 0; e < V; ++e) sum[e] += old[e];
     }
-    store_values<V, kTableF32>(a.table, i, sum);
-}
-
-// One wave per table row; rows of long runs are left to the join.
-template <int V, bool kRowsF32, bool kTableF32>
-__global__ void __launch_bounds__(256) embed_grad_rows_kernel(const GradArgs a)
-{
-    const uint32_t v = uniform(blockIdx.x * 4 + (threadIdx.x >> 6)), lane = threadIdx.x & 63u;
-    if (v >= a.vocab) return;
-    const uint32_t first = uniform(find_run(a.keys, a.n, v));
-    const uint64_t at = static_cast<uint64_t>(first) + lane;
-    const bool mine = at < a.n && a.keys[at] == v;
-    const uint32_t count = static_cast<uint32_t>(__popcll(__ballot(mine)));
-    if (count > kRun || (count == 0 && a.add)) return;
-    for (uint32_t c = lane * V; c < a.width; c += 64 * V) {
-        float sum[V];
-        sum_rows<V, kRowsF32>(a, first, count, c, sum);
-        put_gradient<V, kTableF32>(a, v, c, sum);
-    }
+    store_values<V, kTableF32, false>(a.table, i, sum);
 }
 
 // The runs at the two ends of block b of kRun sorted positions.  first_*:
@@ -376,11 +425,33 @@ __device__ __forceinline__ BlockRuns block_runs(const GradArgs& a, uint32_t b)
     return r;
 }
 
-template <int V, bool kRowsF32>
-__global__ void __launch_bounds__(256) embed_grad_parts_kernel(const GradArgs a, uint32_t chunks)
+// A wave writes some table rows; rows of long runs are left to the join.
+template <int V, bool kRowsF32, bool kTableF32, bool kOnce>
+__device__ __forceinline__ void grad_rows(const GradArgs& a, uint32_t v0, uint32_t rows)
+{
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t v1 = a.vocab - v0 < rows ? a.vocab : v0 + rows;
+    uint32_t first = uniform(find_run(a.keys, a.n, v0));
+    for (uint32_t v = v0; v < v1; ++v) {
+        const uint64_t at = static_cast<uint64_t>(first) + lane;
+        const uint32_t key = at < a.n ? a.keys[at] : 0xFFFFFFFFu;
+        uint32_t count = static_cast<uint32_t>(__popcll(__ballot(key == v)));
+        if (count <= kRun && !(count == 0 && a.add)) {
+            for (uint32_t c = lane * V; c < a.width; c += 64 * V) {
+                float sum[V];
+                sum_rows<V, kRowsF32, kOnce>(a, first, count, c, sum);
+                put_gradient<V, kTableF32>(a, v, c, sum);
+            }
+        }
+        if (count < 64) first += count;
+        else if (v + 1 < v1) first = uniform(find_run(a.keys, a.n, v + 1));
+    }
+}
+
+template <int V, bool kRowsF32, bool kOnce>
+__device__ __forceinline__ void grad_parts(const GradArgs& a, uint64_t job, uint32_t chunks)
 {
     static_assert(kRun == 32, "block_runs looks at half a wave");
-    const uint64_t job = static_cast<uint64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
     const uint64_t b = job / chunks;
     if (b * kRun >= a.n) return;
     const BlockRuns r = block_runs(a, static_cast<uint32_t>(b));
@@ -391,9 +462,23 @@ __global__ void __launch_bounds__(256) embed_grad_parts_kernel(const GradArgs a,
         const uint32_t first = uniform(static_cast<uint32_t>(b) * kRun + r.begin[x]), count = uniform(r.count[x]);
         if (c >= a.width) continue;
         float sum[V];
-        sum_rows<V, kRowsF32>(a, first, count, c, sum);
-        store_values<V, true>(a.parts, (b * 2 + x) * static_cast<uint64_t>(a.width) + c, sum);
+        sum_rows<V, kRowsF32, kOnce>(a, first, count, c, sum);
+        store_values<V, true, false>(a.parts, (b * 2 + x) * static_cast<uint64_t>(a.width) + c, sum);
     }
+}
+
+// The rows of the table, and in the same launch the parts of long runs:
+// part_groups workgroups of parts first, which take longest.
+template <int V, bool kRowsF32, bool kTableF32, bool kOnce>
+__global__ void __launch_bounds__(256) embed_grad_kernel(const GradArgs a, uint32_t part_groups, uint32_t chunks, uint32_t rows_per_wave)
+{
+    const uint32_t wave = uniform(threadIdx.x >> 6);
+    if (blockIdx.x < part_groups) {
+        grad_parts<V, kRowsF32, kOnce>(a, static_cast<uint64_t>(blockIdx.x) * 4 + wave, chunks);
+        return;
+    }
+    const uint64_t v0 = (static_cast<uint64_t>(blockIdx.x - part_groups) * 4 + wave) * rows_per_wave;
+    if (v0 < a.vocab) grad_rows<V, kRowsF32, kTableF32, kOnce>(a, static_cast<uint32_t>(v0), rows_per_wave);
 }
 
 // The parts of a long run, joined in order by the block it starts in: four
@@ -418,7 +503,7 @@ __global__ void __launch_bounds__(256) embed_grad_join_kernel(const GradArgs a, 
 #pragma unroll 4
         for (uint32_t k = k0; k < k1; ++k) {
             float p[V];
-            load_values<V, true>(a.parts, ((static_cast<uint64_t>(b) + k) * 2 + (k == 0 ? x : 0)) * a.width + c, p);
+            load_values<V, true, false>(a.parts, ((static_cast<uint64_t>(b) + k) * 2 + (k == 0 ? x : 0)) * a.width + c, p);
 #pragma unroll
             for (int e = 0; e < V; ++e) sum[e] += p[e];
         }
@@ -497,6 +582,11 @@ Tokens tokens_of(const lso_embed& e)
     return {e.tokens, static_cast<uint32_t>(e.n), static_cast<uint32_t>(e.vocab), e.token_dtype == LSO_DT_I64};
 }
 
+// Table rows per wave of the gradient: several where most rows are empty.
+uint32_t rows_of_wave(uint64_t n, uint64_t vocab) { return n * 4 <= vocab ? 4 : 1; }
+
+bool beyond_l2(const lso_embed& e) { return e.n * e.width * elem_bytes(e.rows_dtype) > kL2Bytes; }
+
 // Eight values per lane, if every row starts on 16 bytes.
 bool vectors(const lso_embed& e)
 {
@@ -525,33 +615,42 @@ lso_status launch_lookup(const lso_embed& e, hipStream_t s)
     if (groups > kMaxGroups) return too_large();
     const dim3 grid(static_cast<uint32_t>(groups)), threads(256);
     const bool t32 = e.table_dtype == LSO_DT_F32, r32 = e.rows_dtype == LSO_DT_F32;
-    if (t32 && r32) hipLaunchKernelGGL((embed_lookup_kernel<V, true, true>), grid, threads, 0, s, a);
-    else if (t32) hipLaunchKernelGGL((embed_lookup_kernel<V, true, false>), grid, threads, 0, s, a);
-    else if (r32) hipLaunchKernelGGL((embed_lookup_kernel<V, false, true>), grid, threads, 0, s, a);
-    else hipLaunchKernelGGL((embed_lookup_kernel<V, false, false>), grid, threads, 0, s, a);
+    auto launch = [&](auto once) {
+        constexpr bool kOnce = decltype(once)::value;
+        if (t32 && r32) hipLaunchKernelGGL((embed_lookup_kernel<V, true, true, kOnce>), grid, threads, 0, s, a);
+        else if (t32) hipLaunchKernelGGL((embed_lookup_kernel<V, true, false, kOnce>), grid, threads, 0, s, a);
+        else if (r32) hipLaunchKernelGGL((embed_lookup_kernel<V, false, true, kOnce>), grid, threads, 0, s, a);
+        else hipLaunchKernelGGL((embed_lookup_kernel<V, false, false, kOnce>), grid, threads, 0, s, a);
+    };
+    if (beyond_l2(e)) launch(std::true_type{});
+    else launch(std::false_type{});
     const hipError_t err = hipGetLastError();
     return err == hipSuccess ? LSO_OK : hip_fail(err, "embedding lookup launch");
 }
 
 template <int V, bool kRowsF32, bool kTableF32>
-void launch_grad_typed(const GradArgs& a, hipStream_t s)
+void launch_grad_typed(const GradArgs& a, bool once, hipStream_t s)
 {
     const dim3 threads(256);
-    hipLaunchKernelGGL((embed_grad_rows_kernel<V, kRowsF32, kTableF32>), dim3((a.vocab + 3) / 4), threads, 0, s, a);
-    if (a.n <= kRun) return;
-    const uint32_t blocks = (a.n + kRun - 1) / kRun, chunks = (a.width + 64 * V - 1) / (64 * V);
-    const uint64_t jobs = static_cast<uint64_t>(blocks) * chunks;
-    hipLaunchKernelGGL((embed_grad_parts_kernel<V, kRowsF32>), dim3(static_cast<uint32_t>((jobs + 3) / 4)), threads, 0, s, a, chunks);
-    hipLaunchKernelGGL((embed_grad_join_kernel<V, kTableF32>), dim3(static_cast<uint32_t>(jobs)), threads, 0, s, a, chunks);
+    const uint32_t rows_per_wave = rows_of_wave(a.n, a.vocab), row_groups = (a.vocab + 4 * rows_per_wave - 1) / (4 * rows_per_wave);
+    const uint32_t blocks = a.n > kRun ? (a.n + kRun - 1) / kRun : 0;   // a run of up to kRun is no long one
+    const uint32_t chunks = (a.width + 64 * V - 1) / (64 * V);
+    const uint32_t jobs = blocks * chunks, part_groups = (jobs + 3) / 4;
+    const dim3 grid(part_groups + row_groups);
+    if (once)
+        hipLaunchKernelGGL((embed_grad_kernel<V, kRowsF32, kTableF32, true>), grid, threads, 0, s, a, part_groups, chunks, rows_per_wave);
+    else
+        hipLaunchKernelGGL((embed_grad_kernel<V, kRowsF32, kTableF32, false>), grid, threads, 0, s, a, part_groups, chunks, rows_per_wave);
+    if (blocks > 0) hipLaunchKernelGGL((embed_grad_join_kernel<V, kTableF32>), dim3(jobs), threads, 0, s, a, chunks);
 }
 
 template <int V>
-void launch_grad(const GradArgs& a, bool r32, bool t32, hipStream_t s)
+void launch_grad(const GradArgs& a, bool r32, bool t32, bool once, hipStream_t s)
 {
-    if (r32 && t32) launch_grad_typed<V, true, true>(a, s);
-    else if (r32) launch_grad_typed<V, true, false>(a, s);
-    else if (t32) launch_grad_typed<V, false, true>(a, s);
-    else launch_grad_typed<V, false, false>(a, s);
+    if (r32 && t32) launch_grad_typed<V, true, true>(a, once, s);
+    else if (r32) launch_grad_typed<V, true, false>(a, once, s);
+    else if (t32) launch_grad_typed<V, false, true>(a, once, s);
+    else launch_grad_typed<V, false, false>(a, once, s);
 }
 
 // Sort the tokens into workspace; sets a.keys and a.pos.
@@ -559,6 +658,16 @@ void launch_sort(const lso_embed& e, char* work, const GradWork& w, GradArgs& a,
 {
     uint32_t bits = 1;
     while ((e.vocab >> bits) != 0) ++bits;   // the largest key is vocab
+    if (e.n <= kRankSort) {
+        RankArgs x{};
+        x.tokens = tokens_of(e);
+        x.keys_out = reinterpret_cast<uint32_t*>(work + w.keys[0]);
+        x.pos_out = reinterpret_cast<uint32_t*>(work + w.pos[0]);
+        hipLaunchKernelGGL(sort_by_rank_kernel, dim3((x.tokens.n + 63) / 64), dim3(1024), 0, s, x);
+        a.keys = x.keys_out;
+        a.pos = x.pos_out;
+        return;
+    }
     const uint32_t passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
     SortArgs x{};
     x.tokens = tokens_of(e);
@@ -617,7 +726,7 @@ lso_status gradient(const lso_embed* e, void* workspace, uint64_t workspace_byte
     if (st != LSO_OK) return st;
     const bool vec = vectors(*e);
     const uint64_t columns = (e->width + (vec ? 511 : 63)) / (vec ? 512 : 64);   // column runs of a wave
-    if (e->vocab / 4 + 1 > kMaxGroups || (e->n + kRun - 1) / kRun * columns > kMaxGroups) return too_large();
+    if (e->vocab / (4 * rows_of_wave(e->n, e->vocab)) + 1 + (e->n + kRun - 1) / kRun * columns > kMaxGroups) return too_large();
     hipStream_t s = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();   // an error left by other work is not this call's
     char* work = static_cast<char*>(workspace);
@@ -634,8 +743,8 @@ lso_status gradient(const lso_embed* e, void* workspace, uint64_t workspace_byte
     a.add = (e->flags & LSO_EMBED_ADD) != 0;
     if (e->n > 0) launch_sort(*e, work, w, a, s);
     const bool r32 = e->rows_dtype == LSO_DT_F32, t32 = e->table_dtype == LSO_DT_F32;
-    if (vec) launch_grad<8>(a, r32, t32, s);
-    else launch_grad<1>(a, r32, t32, s);
+    if (vec) launch_grad<8>(a, r32, t32, beyond_l2(*e), s);
+    else launch_grad<1>(a, r32, t32, false, s);
     const hipError_t err = hipGetLastError();
     return err == hipSuccess ? LSO_OK : hip_fail(err, "embedding gradient launch");
 }

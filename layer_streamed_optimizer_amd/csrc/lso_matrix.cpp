@@ -2,7 +2,6 @@
 // plan and the table of a call.
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 #include <new>
 #include <vector>
 
@@ -208,7 +207,10 @@ lso_status collect(const lso_muon_block* blocks, size_t n, std::vector<Item>& it
 struct Tiles {
     uint64_t count, stages;   // of one matrix in one launch
 };
-constexpr uint64_t kPartCost = 16;
+// kPartCost: measured over calls of one to four matrices of 64 x 2048 to 4096 x 4096:
+// 8 and 16 cut too finely (1024 x 1024 half precision 243 against 178 us with
+// 64), 32 and 128 are within 3% of 64.
+constexpr uint64_t kPartCost = 64;
 
 uint64_t units_of(const std::vector<Tiles>& list, uint64_t depth)
 {
@@ -235,15 +237,20 @@ uint32_t part_depth(const std::vector<Tiles>& list, uint64_t slots)
     return static_cast<uint32_t>(best);
 }
 
+// The edge of the products' tiles.  Large tiles load less per operation, small
+// ones fill the 256 CUs and the pipeline with less work.  By the operations
+// of a step; measured (us, edges 64 / 128 / 256): 22 of 256 x 2048 in half
+// precision (0.9e10) 290 / 369 / 470; in full precision 1024 x 4096 (1.4e10) 416 /
+// 535 / 1305, 2048 x 2048 (3.4e10) 725 / 700 / 1373, three of 2048 x 5632
+// (2.4e11) 4526 / 3693 / 3951, 4096 x 4096 (2.7e11) 4787 / 4092 / 3761.
 uint32_t tile_edge(const std::vector<Item>& items)
 {
-    uint64_t tiles = 0;
+    double work = 0.0;
     for (const Item& it : items) {
         const uint64_t k = std::min(it.rows, it.cols), l = std::max(it.rows, it.cols);
-        if (small_class(k) < 0) tiles += padded(k, 256) / 256 * (padded(l, 256) / 256);
+        if (small_class(k) < 0) work += static_cast<double>(k) * k * (3.0 * l + k);
     }
-    if (const char* e = std::getenv("NS_EDGE")) return std::atoi(e);
-    return tiles >= 512 ? 256 : tiles >= 256 ? 128 : 64;
+    return work >= 2.6e11 ? 256 : work >= 3e10 ? 128 : 64;
 }
 
 // Order the items (small path by class, then the general path, deep matrices

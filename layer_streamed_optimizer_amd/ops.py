@@ -24,13 +24,18 @@ MATRIX_DTYPE = np.dtype(LsoMatrix)
 MUON_DTYPE = np.dtype(LsoMuonBlock)
 
 
+_codes: dict = {}
+
+
 def dtype_of(tensor) -> int:
     """The LSO_DT_* code of a torch tensor's dtype."""
-    import torch
-    codes = {torch.float32: LSO_DT_F32, torch.bfloat16: LSO_DT_BF16, torch.int32: LSO_DT_I32, torch.int64: LSO_DT_I64}
-    if tensor.dtype not in codes:
-        raise TypeError(f"dtype {tensor.dtype} is not one of {', '.join(str(d) for d in codes)}")
-    return codes[tensor.dtype]
+    if not _codes:
+        import torch
+        _codes.update({torch.float32: LSO_DT_F32, torch.bfloat16: LSO_DT_BF16, torch.int32: LSO_DT_I32, torch.int64: LSO_DT_I64})
+    code = _codes.get(tensor.dtype)
+    if code is None:
+        raise TypeError(f"dtype {tensor.dtype} is not one of {', '.join(str(d) for d in _codes)}")
+    return code
 
 
 class _Table:
@@ -154,12 +159,6 @@ def muon_step(table: MuonTable, workspace, workspace_bytes: int, *, steps: int =
 
 # ------------------------------------------------------------------ embedding
 
-def _on_current(device) -> None:
-    import torch
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, which is not the current device")
-
-
 def _embed(tokens, table, rows, scale: float, flags: int) -> LsoEmbed:
     """The descriptor of torch tensors: tokens (any shape, contiguous), table
     [vocab, width], rows [..., width] with one position after another."""
@@ -172,28 +171,31 @@ def _embed(tokens, table, rows, scale: float, flags: int) -> LsoEmbed:
         raise ValueError(f"rows of shape {tuple(rows.shape)} do not match {n} tokens of width {width}")
     if rows.dim() != 2:
         rows = rows.view(n, width)   # raises if the positions are not evenly spaced
-    for name, t in (("table", table), ("rows", rows)):
-        if t.shape[1] > 1 and t.shape[0] > 0 and t.stride(1) != 1:
-            raise ValueError(f"{name}: the elements of a row must be contiguous")
-    devices = {t.device for t in (tokens, table, rows)}
-    if len(devices) != 1 or next(iter(devices)).type != "cuda":
+    ld_table, in_table = table.stride()
+    ld_rows, in_rows = rows.stride()
+    if width > 1 and ((vocab > 0 and in_table != 1) or (n > 0 and in_rows != 1)):
+        raise ValueError("the elements of a row must be contiguous")
+    device = tokens.device
+    if device.type != "cuda" or table.device != device or rows.device != device:
         raise ValueError("tokens, table and rows must be on one GPU")
-    _on_current(tokens.device)
-    e = LsoEmbed()
-    e.tokens, e.n, e.token_dtype = tokens.data_ptr() or None, n, dtype_of(tokens)
-    e.table, e.vocab, e.width, e.table_dtype = table.data_ptr() or None, vocab, width, dtype_of(table)
-    e.ld_table = table.stride(0) if vocab > 1 else width
-    e.rows, e.rows_dtype = rows.data_ptr() or None, dtype_of(rows)
-    e.ld_rows = rows.stride(0) if n > 1 else width
-    e.flags, e.scale = flags, scale
-    return e
+    import torch
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current device")
+    return LsoEmbed(tokens.data_ptr(), n, table.data_ptr(), vocab, width, ld_table if vocab > 1 else width, rows.data_ptr(),
+                    ld_rows if n > 1 else width, dtype_of(tokens), dtype_of(table), dtype_of(rows), flags, scale)
+
+
+_lookup_fn = None
 
 
 def embed_lookup(tokens, weight, out, *, scale: float = 1.0, stream=None) -> None:
     """out[i] = scale * weight[tokens[i]] (a zero row where the token is
     outside the table).  Torch tensors; asynchronous."""
+    global _lookup_fn
+    if _lookup_fn is None:
+        _lookup_fn = _native.lib().lso_embed_lookup
     e = _embed(tokens, weight, out, scale, 0)
-    st = _native.lib().lso_embed_lookup(ctypes.byref(e), stream_handle(stream))
+    st = _lookup_fn(ctypes.byref(e), stream_handle(stream))
     if st:
         _native.check(st, "lso_embed_lookup")
 
