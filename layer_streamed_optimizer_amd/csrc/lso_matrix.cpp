@@ -28,15 +28,21 @@ int small_class(uint64_t k) { return k <= 8 ? 0 : k <= 16 ? 1 : k <= LSO_NS_SMAL
 
 // The largest values that a run from s <= 1 can meet: of the iterates'
 // singular values s, of s^2 and of the polynomial a + b s^2 + c s^4; and for
-// each step the power of two that the polynomial stays under.
-double most_value(const double* coef, uint32_t steps, uint32_t* shift)
+// each step the power of two that the polynomial stays under, and whether it
+// and the next step's may be multiplied with each other (and with S).
+double most_value(const double* coef, uint32_t steps, uint32_t* shift, bool* pair)
 {
-    double s = 1.0, most = 1.0;
+    double s = 1.0, most = 1.0, poly_before = 0.0;
+    bool alone = false;
     for (uint32_t k = 0; k < steps; ++k) {
         const double a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2], z = s * s;
         double poly = std::max(std::fabs(a), std::fabs(a + b * z + c * z * z));
         if (c != 0.0 && -b / (2 * c) > 0.0 && -b / (2 * c) < z) poly = std::max(poly, std::fabs(a - b * b / (4 * c)));
         most = std::max({most, z, poly});
+        if (k > 0) pair[k - 1] = !alone && poly_before * poly <= kNsMostValue;
+        alone = !(poly * z <= kNsMostValue);
+        poly_before = poly;
+        pair[k] = false;
         shift[k] = 0;
         while (shift[k] < 4 && poly >= std::ldexp(1.0, static_cast<int>(shift[k]))) ++shift[k];
         // s p(s^2) on [0, s]: at the end, and where 5 c t^2 + 3 b t + a = 0, t = s^2
@@ -68,7 +74,7 @@ lso_status check_params(const lso_ns_params* p, NsCall& c)
         c.coef[k] = p && p->coef ? p->coef[k] : kDefaultCoef[k % 3];
         if (!std::isfinite(c.coef[k])) return fail(LSO_E_INVALID, "coefficient %u is not finite", k);
     }
-    const double most = most_value(c.coef, c.steps, c.shift);
+    const double most = most_value(c.coef, c.steps, c.shift, c.pair);
     if (!(most <= kNsMostValue))
         return fail(LSO_E_INVALID, "the coefficients let a value reach %.3g, more than %.3g", most, kNsMostValue);
     return LSO_OK;
@@ -253,6 +259,30 @@ uint32_t tile_edge(const std::vector<Item>& items)
     return work >= 2.6e11 ? 256 : work >= 3e10 ? 128 : 64;
 }
 
+// How the call's numbers are held, and whether steps are taken in pairs:
+// X_{k+2} = Q X_k with Q = P' P, P' the polynomial in S' = P S P.  A step by
+// itself makes S = X X^T (half of it, m^2 n operations), S^2 (m^3) and P X (2 m^2 n); a
+// pair makes S, Q X and five products of m x m, so it saves 3 m^2 n - 3 m^3
+// of 6 m^2 n + 2 m^3.  It loses no accuracy: S' is as far from the product of
+// the next X with itself as rounding makes that one.  In half precision the
+// squares keep two terms then (with one the error grows, with two it falls
+// below that of single steps), which costs three products for each one.
+// PAIRS_MEASURED
+NsLayout layout_of(const lso_ns_params* p, bool all_bf16, const std::vector<Item>& items, NsCall& c)
+{
+    const uint32_t precision = p ? p->precision : LSO_NS_AUTO;
+    const uint32_t terms = precision == LSO_NS_FULL || (precision == LSO_NS_AUTO && !all_bf16) ? 2 : 1;
+    double single = 0.0, pair = 0.0;   // matrix-core products of two steps
+    for (const Item& it : items) {
+        const double m = static_cast<double>(std::min(it.rows, it.cols)), n = static_cast<double>(std::max(it.rows, it.cols));
+        if (small_class(std::min(it.rows, it.cols)) >= 0) continue;
+        single += terms == 2 ? 3 * (6 * m * m * n + 2 * m * m * m) : 10 * m * m * n + 2 * m * m * m;
+        pair += terms == 2 ? 3 * (3 * m * m * n + 5 * m * m * m) : 5 * m * m * n + 15 * m * m * m;
+    }
+    c.pairs = pair * 1.1 < single;   // whatever the steps: the workspace depends on sizes, types and precision alone
+    return c.pairs ? NsLayout{terms, 2, 4} : NsLayout{terms, terms, 2};
+}
+
 // Order the items (small path by class, then the general path, deep matrices
 // first), give each its part of the workspace and its first index in every
 // launch.  work is the workspace's address (0 to plan only); returns the
@@ -297,10 +327,10 @@ uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<N
                 m.np = static_cast<uint32_t>(np);
                 m.prep0 = static_cast<uint32_t>(prep);
                 prep += mp / kNsPrep * (np / kNsPrep);
-                at += ns_work(mp, np, c.gram_terms).bytes;
-                const uint64_t values = c.gram_terms == 1 ? 32 : 16;   // of the summed index per stage
-                lists[0].push_back({tm * (tm + 1) / 2, np / values});
-                lists[1].push_back({tm * (tm + 1) / 2, mp / values});
+                at += ns_work(mp, np, c.layout).bytes;
+                // stages hold 16 values of the summed index, 32 where both operands have one term
+                lists[0].push_back({tm * (tm + 1) / 2, np / (c.layout.x_terms == 1 ? 32 : 16)});
+                lists[1].push_back({tm * (tm + 1) / 2, mp / (c.layout.square_terms == 1 ? 32 : 16)});
                 lists[2].push_back({tm * tn, mp / 16});
                 lists[3].push_back({tm * tn, mp / 32});
             }
@@ -317,8 +347,8 @@ uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<N
         }
     }
     if (c.nbig > 0) {
-        NsProduct* products[4] = {&c.gram, &c.poly, &c.apply, &c.apply_one};
-        uint32_t NsMat::*firsts[4] = {&NsMat::gram0, &NsMat::poly0, &NsMat::apply0, &NsMat::apply_one0};
+        NsProduct* products[4] = {&c.gram, &c.square, &c.apply, &c.apply_one};
+        uint32_t NsMat::*firsts[4] = {&NsMat::gram0, &NsMat::square0, &NsMat::apply0, &NsMat::apply_one0};
         uint64_t most_units = 0, part_units = 0;
         for (int p = 0; p < 4; ++p) {
             const uint64_t units_before = units_of(lists[p], UINT32_MAX);
@@ -354,12 +384,6 @@ uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<N
     return at;
 }
 
-uint32_t gram_terms(const lso_ns_params* p, bool all_bf16)
-{
-    const uint32_t precision = p ? p->precision : LSO_NS_AUTO;
-    if (precision == LSO_NS_AUTO) return all_bf16 ? 1 : 2;
-    return precision == LSO_NS_HALF ? 1 : 2;
-}
 
 template <typename T>
 uint64_t workspace_bytes(const T* list, size_t n, const lso_ns_params* params)
@@ -370,7 +394,7 @@ uint64_t workspace_bytes(const T* list, size_t n, const lso_ns_params* params)
     std::vector<NsMat> table;
     bool all_bf16;
     if (check_params(params, c) != LSO_OK || collect(list, n, items, nullptr, all_bf16) != LSO_OK) return 0;
-    c.gram_terms = gram_terms(params, all_bf16);
+    c.layout = layout_of(params, all_bf16, items, c);
     return plan(items, c, 0, table);
 }
 
@@ -387,7 +411,7 @@ lso_status run(const T* list, size_t n, const lso_ns_params* params, void* works
     if (s == LSO_OK) s = collect(list, n, items, &iv, all_bf16);
     if (s != LSO_OK) return s;
     if (items.empty()) return LSO_OK;
-    c.gram_terms = gram_terms(params, all_bf16);
+    c.layout = layout_of(params, all_bf16, items, c);
     if (!workspace) return fail(LSO_E_INVALID, "workspace is NULL");
     if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return fail(LSO_E_ALIGN, "workspace must be 16-byte aligned");
     const uint64_t need = plan(items, c, reinterpret_cast<uintptr_t>(workspace), table);

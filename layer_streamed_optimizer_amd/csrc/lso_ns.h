@@ -47,32 +47,37 @@ struct NsMat {
     // first index of this matrix in the index space of each launch
     uint32_t prep0;     // kNsPrep tiles of the padded matrix; small path: chunks
     uint32_t gram0;     // units (tile, part of the summed index) of S, a multiple of 8 per matrix
-    uint32_t poly0;     // of the polynomial
+    uint32_t square0;   // of a product of two squares
     uint32_t apply0;    // of X
     uint32_t apply_one0;   // of X where X^T has one term
 };
 static_assert(sizeof(NsMat) == 104, "NsMat layout");
 
-// Offsets of a general-path matrix inside its part of the workspace:
-// X (smaller side by larger, gram_terms FP16 numbers per value, read by the
-// product S = X X^T), its transpose twice (up to two numbers per value, read
-// and written in turn by the product with the polynomial P), S and P.
+// What a call's workspace holds per value: X (the smaller side by the larger,
+// read by S = X X^T) in x_terms FP16 numbers, its transpose (read and written
+// in turn by the product with the polynomial) in up to two, and `squares`
+// matrices of the smaller side in square_terms.
+struct NsLayout {
+    uint32_t x_terms, square_terms, squares;
+};
+
+// Offsets of a general-path matrix inside its part of the workspace.
 struct NsWork {
-    uint64_t x, xt[2], s, p, partial, inv, bytes;
+    uint64_t x, xt[2], square, square_bytes, partial, inv, bytes;
 };
 #if defined(__HIPCC__)
 __host__ __device__
 #endif
-inline NsWork ns_work(uint64_t mp, uint64_t np, uint64_t gram_terms)
+inline NsWork ns_work(uint64_t mp, uint64_t np, const NsLayout& l)
 {
-    const uint64_t xs = mp * np * 2, ss = mp * mp * 2 * gram_terms;   // multiples of 256
+    const uint64_t xs = mp * np * 2;   // all of these are multiples of 256
     NsWork w{};
     w.x = 0;
-    w.xt[0] = xs * gram_terms;
+    w.xt[0] = xs * l.x_terms;
     w.xt[1] = w.xt[0] + 2 * xs;
-    w.s = w.xt[1] + 2 * xs;
-    w.p = w.s + ss;
-    w.inv = w.p + ss;
+    w.square = w.xt[1] + 2 * xs;
+    w.square_bytes = mp * mp * 2 * l.square_terms;
+    w.inv = w.square + w.square_bytes * l.squares;
     w.partial = w.inv + 256;
     w.bytes = w.partial + (mp / kNsPrep * (np / kNsPrep) * 8 + 255) / 256 * 256;
     return w;
@@ -98,12 +103,14 @@ struct NsCall {
     uint32_t nsmall[kNsClasses], nbig;
     uint32_t small_chunks[kNsClasses];     // index spaces
     uint32_t prep_tiles;
-    NsProduct gram, poly, apply, apply_one;
+    NsProduct gram, square, apply, apply_one;
     uint32_t tile;                         // edge of a product tile: 64, 128 or 256
     float* parts;                          // workspace of the parts' sums
     uint32_t* counters;
     uint32_t ncounters;
-    uint32_t gram_terms;                   // 1 or 2
+    NsLayout layout;
+    bool pairs;                            // take steps two at a time where pair[] allows
+    bool pair[kNsMaxSteps];                // step k and the next one may be taken together
     uint32_t steps;
     double eps;
     double coef[3 * kNsMaxSteps];

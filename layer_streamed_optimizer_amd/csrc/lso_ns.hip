@@ -227,7 +227,7 @@ __device__ __forceinline__ void prep_tile(const NsMat& m, uint32_t t, uint32_t& 
     c0 = t % across * kNsPrep;
 }
 
-__global__ void __launch_bounds__(256) ns_norm_kernel(const NsMat* tab, uint32_t n, uint32_t gram_terms, uint32_t* counters,
+__global__ void __launch_bounds__(256) ns_norm_kernel(const NsMat* tab, uint32_t n, NsLayout layout, uint32_t* counters,
                                                       uint32_t ncounters)
 {
     // the products' counters start at zero
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const NsMat* tab, uint32_t
         for (int e = 0; e < 4; ++e) sum = fma(static_cast<double>(u[k][e]), static_cast<double>(u[k][e]), sum);
     sum = group_sum<256>(sum);
     if (threadIdx.x == 0) {
-        const NsWork w = ns_work(m.mp, m.np, gram_terms);
+        const NsWork w = ns_work(m.mp, m.np, layout);
         reinterpret_cast<double*>(m.work + w.partial)[blockIdx.x - m.prep0] = sum;
     }
 }
@@ -264,10 +264,10 @@ struct NsScaling {
 };
 
 // One workgroup per matrix.
-__global__ void __launch_bounds__(1024) ns_scale_kernel(const NsMat* tab, uint32_t gram_terms, double eps)
+__global__ void __launch_bounds__(1024) ns_scale_kernel(const NsMat* tab, NsLayout layout, double eps)
 {
     const NsMat m = load_mat(tab, blockIdx.x);
-    const NsWork w = ns_work(m.mp, m.np, gram_terms);
+    const NsWork w = ns_work(m.mp, m.np, layout);
     const uint32_t tiles = m.mp / kNsPrep * (m.np / kNsPrep);
     const double* part = reinterpret_cast<const double*>(m.work + w.partial);
     double sum = 0.0;
@@ -332,13 +332,13 @@ __device__ __forceinline__ void get_terms(const char* base, uint32_t row, uint32
 }
 
 // X_0 and its transpose from u, zeros in the padding.
-template <int kT, int kGramTerms, int kXTerms>
-__global__ void __launch_bounds__(256) ns_split_kernel(const NsMat* tab, uint32_t n)
+template <int kT, int kXTerms, int kXtTerms>
+__global__ void __launch_bounds__(256) ns_split_kernel(const NsMat* tab, uint32_t n, NsLayout layout)
 {
     __shared__ float tile[kNsPrep][kNsPrep + 1];
     const uint32_t i = find_mat<&NsMat::prep0>(tab, n, blockIdx.x);
     const NsMat m = load_mat(tab, i);
-    const NsWork w = ns_work(m.mp, m.np, kGramTerms);
+    const NsWork w = ns_work(m.mp, m.np, layout);
     uint32_t r0, c0;
     prep_tile(m, blockIdx.x - m.prep0, r0, c0);
     const double inv = reinterpret_cast<const NsScaling*>(m.work + w.inv)->inv;
@@ -365,11 +365,11 @@ __global__ void __launch_bounds__(256) ns_split_kernel(const NsMat* tab, uint32_
             b[e] = tile[c + e][r];
         }
         if (tall) {
-            put_terms<kT, kXTerms>(xt, r0 + r, m.mp, c0 + c, a);
-            put_terms<kT, kGramTerms>(x, c0 + r, m.np, r0 + c, b);
+            put_terms<kT, kXtTerms>(xt, r0 + r, m.mp, c0 + c, a);
+            put_terms<kT, kXTerms>(x, c0 + r, m.np, r0 + c, b);
         } else {
-            put_terms<kT, kGramTerms>(x, r0 + r, m.np, c0 + c, a);
-            put_terms<kT, kXTerms>(xt, c0 + r, m.mp, r0 + c, b);
+            put_terms<kT, kXTerms>(x, r0 + r, m.np, c0 + c, a);
+            put_terms<kT, kXtTerms>(xt, c0 + r, m.mp, r0 + c, b);
         }
     }
 }
@@ -511,17 +511,21 @@ __device__ __forceinline__ void wait_loads_and_meet()
     meet();
 }
 
-// kApply leaves X^T in as many terms as it reads, kFewer in one.
-enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3, kFewer = 4 };
+// What a product makes: S of X (kGram), a I + b S + c S^2 of S (kPoly), the
+// product of two squares that commute (kSquare; symmetric like them), the
+// next X and its transpose (kApply), or the result (kLast).
+enum { kGram, kPoly, kSquare, kApply, kLast };
 
 struct ProductArgs {
     const NsMat* tab;
     float* parts;        // sums of the parts, [unit][kT * kT]
     uint32_t* counters;  // finished parts, per tile of the launch; zero between launches
     uint32_t n;
+    NsLayout layout;
     uint32_t turn;       // which transpose of X is read
+    uint32_t a_square, b_square, out_square;   // which squares are read and written
     uint32_t depth;      // stages per part
-    double a, b, c;      // coefficients of the step (kPoly)
+    double ca, cb, cc;   // coefficients of the step (kPoly)
     int lowered, lower;  // by how much the steps before and this one lower e
 };
 
@@ -557,7 +561,7 @@ __device__ __forceinline__ void band_tile(uint32_t k, uint32_t tn, uint32_t tm, 
     ti = 4 * g + at % left;
 }
 
-template <int kT, int kTermsA, int kTermsB, int kKind, int kGramTerms>
+template <int kT, int kTermsA, int kTermsB, int kKind, int kTermsOut>
 __global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(const ProductArgs args)
 {
     constexpr int kWaves = kT == 256 ? 8 : 4, kThreads = kWaves * 64;
@@ -574,34 +578,16 @@ __global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(co
     __shared__ __attribute__((aligned(128))) char lds[kLds];
     __shared__ uint32_t last_part;
 
-    const uint32_t mi = kKind <= kPoly ? (kKind == kGram ? find_mat<&NsMat::gram0>(args.tab, args.n, blockIdx.x)
-                                                         : find_mat<&NsMat::poly0>(args.tab, args.n, blockIdx.x))
-                                       : kTermsA == kTermsB && kGramTerms == 1
-                                             ? find_mat<&NsMat::apply_one0>(args.tab, args.n, blockIdx.x)
-                                             : find_mat<&NsMat::apply0>(args.tab, args.n, blockIdx.x);
-    const NsMat m = load_mat(args.tab, mi);
-    const NsWork w = ns_work(m.mp, m.np, kGramTerms);
-    const char* a;
-    const char* b;
-    uint32_t depth, first, tiles;
-    const uint32_t tm = m.mp / kT, tn = m.np / kT;
-    if (kKind == kGram) {
-        a = b = m.work + w.x;
-        depth = m.np;
-        first = m.gram0;
-        tiles = tm * (tm + 1) / 2;
-    } else if (kKind == kPoly) {
-        a = b = m.work + w.s;
-        depth = m.mp;
-        first = m.poly0;
-        tiles = tm * (tm + 1) / 2;
-    } else {
-        a = m.work + ((args.turn & 1u) ? w.xt[1] : w.xt[0]);
-        b = m.work + w.p;
-        depth = m.mp;
-        first = kTermsA == kTermsB && kGramTerms == 1 ? m.apply_one0 : m.apply0;
-        tiles = tm * tn;
-    }
+    constexpr bool kSym = kKind <= kSquare;        // tiles on and under the diagonal, and their mirror images
+    constexpr bool kOne = kTermsA == 1;            // of an apply: X^T has one term
+    constexpr uint32_t NsMat::*kFirst = kKind == kGram ? &NsMat::gram0 : kSym ? &NsMat::square0 : kOne ? &NsMat::apply_one0 : &NsMat::apply0;
+    const NsMat m = load_mat(args.tab, find_mat<kFirst>(args.tab, args.n, blockIdx.x));
+    const NsWork w = ns_work(m.mp, m.np, args.layout);
+    auto square = [&](uint32_t k) { return m.work + w.square + k * w.square_bytes; };
+    const uint32_t tm = m.mp / kT, tn = m.np / kT, tiles = kSym ? tm * (tm + 1) / 2 : tm * tn, first = m.*kFirst;
+    const uint32_t depth = kKind == kGram ? m.np : m.mp;
+    const char* a = kKind == kGram ? m.work + w.x : kSym ? square(args.a_square) : m.work + ((args.turn & 1u) ? w.xt[1] : w.xt[0]);
+    const char* b = kKind == kGram ? a : square(args.b_square);
     const uint32_t stages = depth / kValues, parts = (stages + args.depth - 1) / args.depth;
     // a matrix has a multiple of eight workgroups, which go round the eight
     // XCDs in turn; consecutive units of a matrix go to one XCD, neighbouring
@@ -611,7 +597,7 @@ __global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(co
     if (unit >= units) return;
     const uint32_t k = unit % tiles, part = unit / tiles;
     uint32_t ti, tj;
-    if (kKind <= kPoly) lower_tile(k, tm, ti, tj);
+    if (kSym) lower_tile(k, tm, ti, tj);
     else band_tile(k, tn, tm, ti, tj);
     const uint32_t i0 = ti * kT, j0 = tj * kT;
     const uint32_t s0 = part * args.depth, s1 = s0 + args.depth < stages ? s0 + args.depth : stages;
@@ -780,9 +766,9 @@ __global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(co
         const int e0 = reinterpret_cast<const NsScaling*>(m.work + w.inv)->e;
         const int before = left_of(e0, args.lowered), after = left_of(e0, args.lowered + args.lower), up = after - before;
         if (kKind == kLast) unscale = ldexpf(1.0f / (kNsScale * kNsScale), -after);
-        ca = static_cast<float>(ldexp(args.a, up));
-        cb = static_cast<float>(ldexp(args.b, up - 2 * before));
-        cc = static_cast<float>(ldexp(args.c, up - 4 * before));
+        ca = static_cast<float>(ldexp(args.ca, up));
+        cb = static_cast<float>(ldexp(args.cb, up - 2 * before));
+        cc = static_cast<float>(ldexp(args.cc, up - 4 * before));
     }
     float* tile = reinterpret_cast<float*>(lds);
     for (uint32_t strip = 0; strip < kT; strip += kStrip) {
@@ -832,19 +818,19 @@ __global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(co
         char* out_rows;      // takes D
         char* out_cols;      // takes D transposed
         uint32_t ld_rows, ld_cols;
-        if (kKind > kPoly) {
+        if (kSym) {
+            out_rows = out_cols = square(args.out_square);
+            ld_rows = ld_cols = m.mp;
+        } else {
             out_rows = m.work + ((args.turn & 1u) ? w.xt[0] : w.xt[1]);
             out_cols = m.work + w.x;
             ld_rows = m.mp;
             ld_cols = m.np;
-        } else {
-            out_rows = out_cols = m.work + (kKind == kGram ? w.s : w.p);
-            ld_rows = ld_cols = m.mp;
         }
         // a I + b S + c S^2 from S^2, at elements (row, c .. c + 7)
         auto polynomial = [&](uint32_t row, uint32_t c, float (&d)[8]) {
             float sv[8];
-            get_terms<kT, kGramTerms>(m.work + w.s, row, m.mp, c, sv);
+            get_terms<kT, kTermsA>(square(args.a_square), row, m.mp, c, sv);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 d[e] = fmaf(cc, d[e], cb * sv[e]);
@@ -859,15 +845,14 @@ __global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(co
 #pragma unroll
                 for (int e = 0; e < 8; ++e) d[e] = tile[r * kPitch + c + e];
                 if (kKind == kPoly) polynomial(is + r, j0 + c, d);
-                if (kKind > kPoly) put_terms<kT, kKind == kFewer ? 1 : kTermsA>(out_rows, is + r, ld_rows, j0 + c, d);
-                else put_terms<kT, kGramTerms>(out_rows, is + r, ld_rows, j0 + c, d);
+                put_terms<kT, kTermsOut>(out_rows, is + r, ld_rows, j0 + c, d);
             }
-            if (kKind > kPoly || ti != tj) {
+            if (!kSym || ti != tj) {
                 const uint32_t c = (v & 1u) * 8 + v / (kT * 2) * 16, r = (v >> 1) % kT;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) d[e] = tile[(c + e) * kPitch + r];
                 if (kKind == kPoly) polynomial(j0 + r, is + c, d);
-                put_terms<kT, kGramTerms>(out_cols, j0 + r, ld_cols, is + c, d);
+                put_terms<kT, kSym ? kTermsOut : kTermsB>(out_cols, j0 + r, ld_cols, is + c, d);   // X in the polynomial's terms
             }
         }
     }
@@ -1140,49 +1125,124 @@ hipError_t launch_small(const NsCall& c, const NsMat* tab, uint32_t n, uint32_t 
     return hipGetLastError();
 }
 
-template <int kT, int kGramTerms>
+// The general path.  kTerms: of X as S reads it, and of what X is multiplied by.
+template <int kT, int kTerms>
+class BigLaunch {
+public:
+    BigLaunch(const NsCall& c, const NsMat* tab, hipStream_t s) : c_(c), s_(s)
+    {
+        args_.tab = tab;
+        args_.parts = c.parts;
+        args_.counters = c.counters;
+        args_.n = c.nbig;
+        args_.layout = c.layout;
+    }
+
+    hipError_t run()
+    {
+        const NsMat* tab = args_.tab;
+        hipLaunchKernelGGL(ns_norm_kernel, dim3(c_.prep_tiles), dim3(256), 0, s_, tab, c_.nbig, c_.layout, c_.counters, c_.ncounters);
+        hipLaunchKernelGGL(ns_scale_kernel, dim3(c_.nbig), dim3(1024), 0, s_, tab, c_.layout, c_.eps);
+        if (xt_terms(0) == 2) hipLaunchKernelGGL((ns_split_kernel<kT, kTerms, 2>), dim3(c_.prep_tiles), dim3(256), 0, s_, tab, c_.nbig, c_.layout);
+        else hipLaunchKernelGGL((ns_split_kernel<kT, kTerms, 1>), dim3(c_.prep_tiles), dim3(256), 0, s_, tab, c_.nbig, c_.layout);
+        for (uint32_t k = 0; k < c_.steps;) {
+            const bool pair = paired(k);
+            gram();
+            poly(k, 0, 1, !pair);
+            if (pair) {
+                square(1, 0, 2, false);        // P S
+                square(2, 1, 0, false);        // S' = P S P
+                poly(k + 1, 0, 3, false);      // P'
+                square(3, 1, 2, true);         // Q = P' P
+            }
+            apply(k, pair ? k + 2 : k + 1, pair ? 2 : 1);
+            k += pair ? 2 : 1;
+        }
+        return hipGetLastError();
+    }
+
+private:
+    bool paired(uint32_t k) const { return c_.pairs && c_.pair[k]; }
+
+    // Terms of X^T where step k reads it.  In half precision the last two
+    // steps, taken singly, read one: what no later step magnifies is below
+    // the rounding of S and the polynomial anyway.
+    int xt_terms(uint32_t k) const { return kTerms == 2 || k + 2 < c_.steps || paired(k) ? 2 : 1; }
+
+    template <int kA, int kB, int kKind, int kOut>
+    void launch(const NsProduct& p)
+    {
+        args_.depth = p.depth;
+        hipLaunchKernelGGL((ns_product_kernel<kT, kA, kB, kKind, kOut>), dim3(p.units), dim3(kT == 256 ? 512 : 256), 0, s_, args_);
+    }
+
+    bool two_term_squares() const { return c_.layout.square_terms == 2; }
+
+    void gram()
+    {
+        args_.out_square = 0;
+        if (kTerms == 1 && !two_term_squares()) launch<kTerms, kTerms, kGram, 1>(c_.gram);
+        else launch<kTerms, kTerms, kGram, 2>(c_.gram);
+    }
+
+    void squares(uint32_t a, uint32_t b, uint32_t out)
+    {
+        args_.a_square = a;
+        args_.b_square = b;
+        args_.out_square = out;
+    }
+
+    // The polynomial of step k in square `in`; multiplier: X is multiplied by it.
+    void poly(uint32_t k, uint32_t in, uint32_t out, bool multiplier)
+    {
+        squares(in, in, out);
+        args_.ca = c_.coef[3 * k];
+        args_.cb = c_.coef[3 * k + 1];
+        args_.cc = c_.coef[3 * k + 2];
+        args_.lowered = 0;
+        for (uint32_t j = 0; j < k; ++j) args_.lowered += static_cast<int>(c_.shift[j]);
+        args_.lower = static_cast<int>(c_.shift[k]);
+        if (!two_term_squares()) launch<1, 1, kPoly, 1>(c_.square);
+        else if (multiplier) launch<2, 2, kPoly, kTerms>(c_.square);
+        else launch<2, 2, kPoly, 2>(c_.square);
+    }
+
+    void square(uint32_t a, uint32_t b, uint32_t out, bool multiplier)
+    {
+        squares(a, b, out);
+        if (multiplier) launch<2, 2, kSquare, kTerms>(c_.square);
+        else launch<2, 2, kSquare, 2>(c_.square);
+    }
+
+    // X of step `next` from that of step k (the poly before has set what
+    // kLast needs of the scaling).
+    void apply(uint32_t k, uint32_t next, uint32_t by)
+    {
+        args_.b_square = by;
+        const int from = xt_terms(k), to = next < c_.steps ? xt_terms(next) : 0;
+        if constexpr (kTerms == 2) {
+            if (to == 0) launch<2, 2, kLast, 1>(c_.apply);
+            else launch<2, 2, kApply, 2>(c_.apply);
+        } else if (from == 2) {
+            if (to == 0) launch<2, 1, kLast, 1>(c_.apply);
+            else if (to == 1) launch<2, 1, kApply, 1>(c_.apply);
+            else launch<2, 1, kApply, 2>(c_.apply);
+        } else {
+            if (to == 0) launch<1, 1, kLast, 1>(c_.apply_one);
+            else launch<1, 1, kApply, 1>(c_.apply_one);
+        }
+        ++args_.turn;
+    }
+
+    const NsCall& c_;
+    hipStream_t s_;
+    ProductArgs args_{};
+};
+
+template <int kT>
 hipError_t launch_big(const NsCall& c, const NsMat* tab, hipStream_t s)
 {
-    const uint32_t n = c.nbig;
-    hipLaunchKernelGGL(ns_norm_kernel, dim3(c.prep_tiles), dim3(256), 0, s, tab, n, c.gram_terms, c.counters, c.ncounters);
-    hipLaunchKernelGGL(ns_scale_kernel, dim3(n), dim3(1024), 0, s, tab, c.gram_terms, c.eps);
-    // X^T keeps its l terms for all but the last two steps (or for all, in full
-    // precision): what a later step does not magnify is below the rounding
-    // of S and P anyway
-    const uint32_t twice = kGramTerms == 2 ? c.steps : c.steps > 2 ? c.steps - 2 : 0;
-    if (twice > 0) hipLaunchKernelGGL((ns_split_kernel<kT, kGramTerms, 2>), dim3(c.prep_tiles), dim3(256), 0, s, tab, n);
-    else hipLaunchKernelGGL((ns_split_kernel<kT, kGramTerms, 1>), dim3(c.prep_tiles), dim3(256), 0, s, tab, n);
-    const dim3 threads(kT == 256 ? 512 : 256);
-    int lowered = 0;
-    for (uint32_t k = 0; k < c.steps; ++k) {
-        ProductArgs args{};
-        args.tab = tab;
-        args.parts = c.parts;
-        args.counters = c.counters;
-        args.n = n;
-        args.turn = k;
-        args.a = c.coef[3 * k];
-        args.b = c.coef[3 * k + 1];
-        args.c = c.coef[3 * k + 2];
-        args.lowered = lowered;
-        args.lower = static_cast<int>(c.shift[k]);
-        lowered += args.lower;
-        args.depth = c.gram.depth;
-        hipLaunchKernelGGL((ns_product_kernel<kT, kGramTerms, kGramTerms, kGram, kGramTerms>), dim3(c.gram.units), threads, 0, s, args);
-        args.depth = c.poly.depth;
-        hipLaunchKernelGGL((ns_product_kernel<kT, kGramTerms, kGramTerms, kPoly, kGramTerms>), dim3(c.poly.units), threads, 0, s, args);
-        // (a stage of one-term operands holds twice the values)
-        const dim3 apply(c.apply.units), apply_one(c.apply_one.units);
-        const bool last = k + 1 == c.steps;
-        args.depth = k < twice ? c.apply.depth : c.apply_one.depth;
-        if (k < twice && last) hipLaunchKernelGGL((ns_product_kernel<kT, 2, kGramTerms, kLast, kGramTerms>), apply, threads, 0, s, args);
-        else if (k + 1 < twice || kGramTerms == 2)
-            hipLaunchKernelGGL((ns_product_kernel<kT, 2, kGramTerms, kApply, kGramTerms>), apply, threads, 0, s, args);
-        else if (k < twice) hipLaunchKernelGGL((ns_product_kernel<kT, 2, 1, kFewer, 1>), apply, threads, 0, s, args);
-        else if (last) hipLaunchKernelGGL((ns_product_kernel<kT, 1, 1, kLast, 1>), apply_one, threads, 0, s, args);
-        else hipLaunchKernelGGL((ns_product_kernel<kT, 1, 1, kApply, 1>), apply_one, threads, 0, s, args);
-    }
-    return hipGetLastError();
+    return c.layout.x_terms == 1 ? BigLaunch<kT, 1>(c, tab, s).run() : BigLaunch<kT, 2>(c, tab, s).run();
 }
 
 }  // namespace
@@ -1207,9 +1267,7 @@ int ns_launch(const NsCall& c, NsMat* device_table, void* stream)
         tab += c.nsmall[k];
     }
     if (err == hipSuccess && c.nbig > 0) {
-        if (c.tile == 256) err = c.gram_terms == 1 ? launch_big<256, 1>(c, tab, s) : launch_big<256, 2>(c, tab, s);
-        else if (c.tile == 64) err = c.gram_terms == 1 ? launch_big<64, 1>(c, tab, s) : launch_big<64, 2>(c, tab, s);
-        else err = c.gram_terms == 1 ? launch_big<128, 1>(c, tab, s) : launch_big<128, 2>(c, tab, s);
+        err = c.tile == 256 ? launch_big<256>(c, tab, s) : c.tile == 128 ? launch_big<128>(c, tab, s) : launch_big<64>(c, tab, s);
     }
     return err;
 }
