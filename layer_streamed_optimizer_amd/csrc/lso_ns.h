@@ -84,16 +84,29 @@ inline NsWork ns_work(uint64_t mp, uint64_t np, const NsLayout& l)
 }
 
 // Of a small-path matrix: the FP64 partial products of each chunk, and the
-// k x k matrix that x is multiplied by.
+// k x k matrix that x is multiplied by, in rows of its class's size.
 inline uint64_t ns_small_bytes(uint64_t k, uint64_t l)
 {
-    const uint64_t chunks = (l + kNsSmallChunk - 1) / kNsSmallChunk;
-    return ((chunks + 1) * k * k * 8 + 255) / 256 * 256;
+    const uint64_t chunks = (l + kNsSmallChunk - 1) / kNsSmallChunk, side = k <= 8 ? 8 : k <= 16 ? 16 : 32;
+    return (chunks * k * k * 8 + side * side * 8 + 255) / 256 * 256;
 }
+
+// Where a launch's workgroups belong: matrices first_mat[r] and on have `each`
+// indices apiece from first[r] on, until the next run starts.  runs == 0: too
+// many runs, the table is searched.
+constexpr int kNsRuns = 8;
+struct NsIndex {
+    uint32_t runs;
+    uint32_t first[kNsRuns], first_mat[kNsRuns], each[kNsRuns];
+};
+
+// Blocks of each operand per stage of a product with tiles of this edge.
+constexpr int ns_blocks(uint32_t edge, bool symmetric, int terms) { return edge == 64 && symmetric && terms == 2 ? 2 : 1; }
 
 // A product's launch: workgroups, and stages of the summed index per part.
 struct NsProduct {
     uint32_t units, depth;
+    NsIndex index;
 };
 
 // One call, as the launches need it.  The table holds the small-path
@@ -102,7 +115,9 @@ struct NsCall {
     const NsMat* table;                    // host copy
     uint32_t nsmall[kNsClasses], nbig;
     uint32_t small_chunks[kNsClasses];     // index spaces
+    NsIndex small_index[kNsClasses];
     uint32_t prep_tiles;
+    NsIndex prep_index;
     NsProduct gram, square, apply, apply_one;
     uint32_t tile;                         // edge of a product tile: 64, 128 or 256
     float* parts;                          // workspace of the parts' sums

@@ -29,6 +29,7 @@ namespace {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef double f64x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
@@ -37,9 +38,9 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // ------------------------------------------------------------- the table
 
 // Written by small kernels whose arguments carry the entries (nothing is read
-// from host memory later): 16 KiB of arguments at a time, or 2 KiB for the
-// few matrices of most calls.  308 matrices: two launches (5 us) against nine of
-// 4 KiB (20 us).
+// from host memory later): 32 KiB of arguments at a time, or 2 KiB for the
+// few matrices of most calls.  308 matrices: one launch against nine of 4 KiB
+// (20 us).
 template <uint32_t kCount>
 struct NsTablePart {
     NsMat* dst;
@@ -47,8 +48,8 @@ struct NsTablePart {
     uint32_t pad;
     NsMat src[kCount];
 };
-constexpr uint32_t kWriteFew = 19, kWriteMany = 157;
-static_assert(sizeof(NsTablePart<kWriteFew>) <= 2048 && sizeof(NsTablePart<kWriteMany>) <= 16384, "writer arguments");
+constexpr uint32_t kWriteFew = 19, kWriteMany = 314;
+static_assert(sizeof(NsTablePart<kWriteFew>) <= 2048 && sizeof(NsTablePart<kWriteMany>) <= 32768, "writer arguments");
 
 template <uint32_t kCount>
 __global__ void __launch_bounds__(64) ns_table_kernel(const NsTablePart<kCount> part)
@@ -73,10 +74,23 @@ __device__ __forceinline__ NsMat load_mat(const NsMat* tab, uint32_t i)
     return *reinterpret_cast<const NsMat*>(reinterpret_cast<const char*>(tab) + static_cast<uint64_t>(i) * sizeof(NsMat));
 }
 
-// The last of n matrices whose first index (field F) is <= index.
+// The matrix that workgroup `index` of a launch belongs to: through the
+// launch's runs of alike matrices, or else the last of n whose first index
+// (field F) is <= index.
 template <uint32_t NsMat::*F>
-__device__ __forceinline__ uint32_t find_mat(const NsMat* tab, uint32_t n, uint32_t index)
+__device__ __forceinline__ uint32_t find_mat(const NsMat* tab, uint32_t n, const NsIndex& x, uint32_t index)
 {
+    if (x.runs > 0) {
+        uint32_t first = x.first[0], mat = x.first_mat[0], each = x.each[0];
+#pragma unroll
+        for (int r = 1; r < kNsRuns; ++r)
+            if (static_cast<uint32_t>(r) < x.runs && x.first[r] <= index) {
+                first = x.first[r];
+                mat = x.first_mat[r];
+                each = x.each[r];
+            }
+        return mat + (index - first) / each;
+    }
     uint32_t lo = 0, hi = n;
     while (hi - lo > 1) {
         const uint32_t mid = (lo + hi) >> 1;
@@ -227,12 +241,12 @@ __device__ __forceinline__ void prep_tile(const NsMat& m, uint32_t t, uint32_t& 
     c0 = t % across * kNsPrep;
 }
 
-__global__ void __launch_bounds__(256) ns_norm_kernel(const NsMat* tab, uint32_t n, NsLayout layout, uint32_t* counters,
+__global__ void __launch_bounds__(256) ns_norm_kernel(const NsMat* tab, uint32_t n, NsIndex index, NsLayout layout, uint32_t* counters,
                                                       uint32_t ncounters)
 {
     // the products' counters start at zero
     for (uint32_t k = blockIdx.x * 256 + threadIdx.x; k < ncounters; k += gridDim.x * 256) counters[k] = 0;
-    const uint32_t i = find_mat<&NsMat::prep0>(tab, n, blockIdx.x);
+    const uint32_t i = find_mat<&NsMat::prep0>(tab, n, index, blockIdx.x);
     const NsMat m = load_mat(tab, i);
     uint32_t r0, c0;
     prep_tile(m, blockIdx.x - m.prep0, r0, c0);
@@ -333,10 +347,10 @@ __device__ __forceinline__ void get_terms(const char* base, uint32_t row, uint32
 
 // X_0 and its transpose from u, zeros in the padding.
 template <int kT, int kXTerms, int kXtTerms>
-__global__ void __launch_bounds__(256) ns_split_kernel(const NsMat* tab, uint32_t n, NsLayout layout)
+__global__ void __launch_bounds__(256) ns_split_kernel(const NsMat* tab, uint32_t n, NsIndex index, NsLayout layout)
 {
     __shared__ float tile[kNsPrep][kNsPrep + 1];
-    const uint32_t i = find_mat<&NsMat::prep0>(tab, n, blockIdx.x);
+    const uint32_t i = find_mat<&NsMat::prep0>(tab, n, index, blockIdx.x);
     const NsMat m = load_mat(tab, i);
     const NsWork w = ns_work(m.mp, m.np, layout);
     uint32_t r0, c0;
@@ -521,6 +535,7 @@ struct ProductArgs {
     float* parts;        // sums of the parts, [unit][kT * kT]
     uint32_t* counters;  // finished parts, per tile of the launch; zero between launches
     uint32_t n;
+    NsIndex index;
     NsLayout layout;
     uint32_t turn;       // which transpose of X is read
     uint32_t a_square, b_square, out_square;   // which squares are read and written
@@ -567,7 +582,12 @@ __global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(co
     constexpr int kWaves = kT == 256 ? 8 : 4, kThreads = kWaves * 64;
     constexpr int kWm = kT / 2, kWn = kT == 256 ? 64 : kT / 2;            // a wave's part of the tile
     constexpr int kX = kWm / 32, kY = kWn / 32;                           // in matrix-core tiles
-    constexpr int kValues = (kTermsA == 1 && kTermsB == 1) ? 32 : 16;     // of the summed index per stage
+    // blocks of each operand in a stage (squares of small calls, whose stages
+    // would be all meetings: 1000 x 777 and smaller 264 against 353 us; tiles of
+    // X come in numbers and want the LDS for more workgroups)
+    constexpr int kParts = ns_blocks(kT, kKind <= kSquare, kTermsA);
+    constexpr int kValues = kParts * ((kTermsA == 1 && kTermsB == 1) ? 32 : 16);   // of the summed index per stage
+    constexpr uint32_t kPartA = kT * 2 * kValues * kTermsA / kParts, kPartB = kT * 2 * kValues * kTermsB / kParts;
     constexpr int kRowA = 32 * kTermsA, kRowB = 32 * kTermsB;             // bytes of a row in a block
     constexpr uint32_t kStageA = kT * 2 * kValues * kTermsA, kStageB = kT * 2 * kValues * kTermsB, kStage = kStageA + kStageB;
     constexpr int kRing = 4;
@@ -581,7 +601,7 @@ __global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(co
     constexpr bool kSym = kKind <= kSquare;        // tiles on and under the diagonal, and their mirror images
     constexpr bool kOne = kTermsA == 1;            // of an apply: X^T has one term
     constexpr uint32_t NsMat::*kFirst = kKind == kGram ? &NsMat::gram0 : kSym ? &NsMat::square0 : kOne ? &NsMat::apply_one0 : &NsMat::apply0;
-    const NsMat m = load_mat(args.tab, find_mat<kFirst>(args.tab, args.n, blockIdx.x));
+    const NsMat m = load_mat(args.tab, find_mat<kFirst>(args.tab, args.n, args.index, blockIdx.x));
     const NsWork w = ns_work(m.mp, m.np, args.layout);
     auto square = [&](uint32_t k) { return m.work + w.square + k * w.square_bytes; };
     const uint32_t tm = m.mp / kT, tn = m.np / kT, tiles = kSym ? tm * (tm + 1) / 2 : tm * tn, first = m.*kFirst;
@@ -634,16 +654,16 @@ __global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(co
     const uint32_t at_a = lds0 + row_a * kRowA + pa * 16, at_b = lds0 + kStageA + row_b * kRowB + pb * 16;
     const uint32_t at_a1 = kTermsA == 2 ? lds0 + row_a * kRowA + (pa ^ 2u) * 16 : at_a + kT * kRowA;
     const uint32_t at_b1 = kTermsB == 2 ? lds0 + kStageA + row_b * kRowB + (pb ^ 2u) * 16 : at_b + kT * kRowB;
-    auto read = [&](uint32_t s) {
-        const uint32_t now = (s % kRing) * kStage;
+    auto read = [&](uint32_t s, uint32_t part) {
+        const uint32_t in_a = (s % kRing) * kStage + part * kPartA, in_b = (s % kRing) * kStage + part * kPartB;
         if constexpr (kNb == 2) {
-            if constexpr (kX == 4) read_4_2<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, now + at_b1, fa, fb);
-            else if constexpr (kX == 1) read_1_2<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, now + at_b1, fa, fb);
-            else read_2_2<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, now + at_b1, fa, fb);
+            if constexpr (kX == 4) read_4_2<32 * kRowA, 32 * kRowB>(in_a + at_a, in_a + at_a1, in_b + at_b, in_b + at_b1, fa, fb);
+            else if constexpr (kX == 1) read_1_2<32 * kRowA, 32 * kRowB>(in_a + at_a, in_a + at_a1, in_b + at_b, in_b + at_b1, fa, fb);
+            else read_2_2<32 * kRowA, 32 * kRowB>(in_a + at_a, in_a + at_a1, in_b + at_b, in_b + at_b1, fa, fb);
         } else {
-            if constexpr (kX == 4) read_4_1<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, fa, fb);
-            else if constexpr (kX == 1) read_1_1<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, fa, fb);
-            else read_2_1<32 * kRowA, 32 * kRowB>(now + at_a, now + at_a1, now + at_b, fa, fb);
+            if constexpr (kX == 4) read_4_1<32 * kRowA, 32 * kRowB>(in_a + at_a, in_a + at_a1, in_b + at_b, fa, fb);
+            else if constexpr (kX == 1) read_1_1<32 * kRowA, 32 * kRowB>(in_a + at_a, in_a + at_a1, in_b + at_b, fa, fb);
+            else read_2_1<32 * kRowA, 32 * kRowB>(in_a + at_a, in_a + at_a1, in_b + at_b, fa, fb);
         }
     };
     auto product = [&](const f16x8 (&x8)[kX], const f16x8 (&y8)[kY]) {
@@ -656,19 +676,19 @@ __global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(co
     // busy, send for stage s.  Sent for beside the reads of LDS, the loads held
     // those up: the matrix cores were busy 58% of the time against 78% now,
     // the product of 8192 x 8192 and 8192 x 28672 took 10.0 against 8.6 ms.
-    auto multiply = [&](uint32_t s) {
+    auto multiply = [&](uint32_t s, bool send) {
         product(fa[0], fb[0]);
         __builtin_amdgcn_sched_barrier(0);
-        load_a(s);
+        if (send) load_a(s);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (kTermsA == 1) {
-            load_b(s);
+            if (send) load_b(s);
             __builtin_amdgcn_sched_barrier(0);
             product(fa[1], fb[1]);                               // the second 16 values
         } else {
             if constexpr (kTermsB == 2) product(fa[0], fb[1]);   // h l
             __builtin_amdgcn_sched_barrier(0);
-            load_b(s);
+            if (send) load_b(s);
             __builtin_amdgcn_sched_barrier(0);
             product(fa[1], fb[0]);                               // l h
         }
@@ -681,8 +701,10 @@ __global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(co
     if (kT < 256) {
         for (uint32_t s = s0; s < s1; ++s) {
             wait_loads_and_meet<2 * kLoads>();   // stage s is here, stage s - 1 has been read
-            read(s);
-            multiply(s + 3);
+            for (int part = 0; part < kParts; ++part) {
+                read(s, part);
+                multiply(s + 3, part == 0);
+            }
         }
     } else {
         // Two waves share a SIMD.  Waves 4 to 7 run one meeting behind waves 0
@@ -694,11 +716,11 @@ __global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(co
         wait_loads_and_meet<2 * kLoads>();
         if (second) meet();
         for (uint32_t s = s0; s < s1; ++s) {
-            read(s);
+            read(s, 0);
             if (second) wait_loads<kLoads>();
             meet();
             __builtin_amdgcn_s_setprio(1);
-            multiply(s + 3);
+            multiply(s + 3, true);
             __builtin_amdgcn_s_setprio(0);
             if (!second) wait_loads<2 * kLoads>();
             meet();
@@ -907,50 +929,64 @@ __device__ __forceinline__ void stage_u(const NsMat& m, uint32_t l0, float* u)
 }
 
 template <int kK>
-__global__ void __launch_bounds__(256) ns_small_gram_kernel(const NsMat* tab, uint32_t n)
+__global__ void __launch_bounds__(256) ns_small_gram_kernel(const NsMat* tab, uint32_t n, NsIndex index)
 {
+    // FP64 matrix instructions: 16 x 16 products of 16 rows by 4 values, the
+    // same register for both operands.  With kK = 8 rows 8 to 15 are the
+    // first eight again at the other half of the chunk; with 32 the tiles
+    // are (0, 0), (0, 1) and (1, 1).  (A thread per product, with FP64 vector
+    // instructions, took 14 against GRAMUS us for 308 adapters: two loads
+    // and two conversions for each.)
+    constexpr int kTiles = kK == 32 ? 3 : 1, kRows = kK == 32 ? 2 : 1;
+    constexpr uint32_t kSpan = kK == 8 ? kNsSmallChunk / 2 : kNsSmallChunk;   // values per row
     __shared__ float u[kK * kSmallPitch];
-    __shared__ double part[256];
-    const NsMat m = load_mat(tab, find_mat<&NsMat::prep0>(tab, n, blockIdx.x));
+    __shared__ double part[kTiles * 4 * 256];   // [tile][wave][row][column]
+    const NsMat m = load_mat(tab, find_mat<&NsMat::prep0>(tab, n, index, blockIdx.x));
     const uint32_t chunk = blockIdx.x - m.prep0, k = m.rows < m.cols ? m.rows : m.cols;
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     stage_u<kK, true>(m, chunk * kNsSmallChunk, u);
     __syncthreads();
-    double* out = reinterpret_cast<double*>(m.work) + static_cast<uint64_t>(chunk) * k * k;
-    if constexpr (kK == 32) {
-        // a thread takes (p, q), (p + 16, q), (p, q + 16) and (p + 16, q + 16)
-        const uint32_t p = threadIdx.x >> 4, q = threadIdx.x & 15u;
-        double s00 = 0.0, s01 = 0.0, s10 = 0.0, s11 = 0.0;
+    f64x4 acc[kTiles] = {};
+    const uint32_t row = lane & 15u, at = wave * (kSpan / 4) + (lane >> 4);
+    const float* from = kK == 8 ? u + (row & 7u) * kSmallPitch + (row >> 3) * kSpan + at : u + row * kSmallPitch + at;
 #pragma unroll 4
-        for (uint32_t x = 0; x < kNsSmallChunk; ++x) {
-            const double a0 = u[p * kSmallPitch + x], a1 = u[(p + 16) * kSmallPitch + x];
-            const double b0 = u[q * kSmallPitch + x], b1 = u[(q + 16) * kSmallPitch + x];
-            s00 = fma(a0, b0, s00);
-            s01 = fma(a0, b1, s01);
-            s10 = fma(a1, b0, s10);
-            s11 = fma(a1, b1, s11);
-        }
-        if (p < k && q < k) out[p * k + q] = s00;
-        if (p < k && q + 16 < k) out[p * k + q + 16] = s01;
-        if (p + 16 < k && q < k) out[(p + 16) * k + q] = s10;
-        if (p + 16 < k && q + 16 < k) out[(p + 16) * k + q + 16] = s11;
-    } else {
-        // 256 / (kK * kK) threads per (p, q), each over its own part of the chunk
-        constexpr uint32_t kSlots = kK * kK, kParts = 256 / kSlots, kLen = kNsSmallChunk / kParts;
-        const uint32_t s = threadIdx.x % kSlots, g = threadIdx.x / kSlots, p = s / kK, q = s % kK;
-        double sum0 = 0.0, sum1 = 0.0;
-#pragma unroll 8
-        for (uint32_t x = g * kLen; x < (g + 1) * kLen; x += 2) {
-            sum0 = fma(static_cast<double>(u[p * kSmallPitch + x]), static_cast<double>(u[q * kSmallPitch + x]), sum0);
-            sum1 = fma(static_cast<double>(u[p * kSmallPitch + x + 1]), static_cast<double>(u[q * kSmallPitch + x + 1]), sum1);
-        }
-        double sum = sum0 + sum1;
-        part[threadIdx.x] = sum;
-        __syncthreads();
-        if (g == 0 && p < k && q < k) {
+    for (uint32_t x = 0; x < kSpan / 4; x += 4) {
+        double a[kRows];
 #pragma unroll
-            for (uint32_t x = 1; x < kParts; ++x) sum += part[x * kSlots + s];
-            out[p * k + q] = sum;
+        for (int r = 0; r < kRows; ++r) a[r] = from[r * 16 * kSmallPitch + x];
+        acc[0] = __builtin_amdgcn_mfma_f64_16x16x4f64(a[0], a[0], acc[0], 0, 0, 0);
+        if constexpr (kRows == 2) {
+            acc[1] = __builtin_amdgcn_mfma_f64_16x16x4f64(a[0], a[1], acc[1], 0, 0, 0);
+            acc[2] = __builtin_amdgcn_mfma_f64_16x16x4f64(a[1], a[1], acc[2], 0, 0, 0);
         }
+    }
+    // element e of lane l: row 4 e + l / 16, column l % 16
+#pragma unroll
+    for (int y = 0; y < kTiles; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[((y * 4 + wave) * 16 + 4 * e + (lane >> 4)) * 16 + (lane & 15u)] = acc[y][e];
+    __syncthreads();
+    double* out = reinterpret_cast<double*>(m.work) + static_cast<uint64_t>(chunk) * k * k;
+    for (uint32_t v = threadIdx.x; v < kK * kK; v += 256) {
+        uint32_t p = v / kK, q = v % kK;
+        if (p >= k || q >= k) continue;
+        uint32_t y = 0, r = p, c = q;
+        if (kK == 32) {
+            if (p > q) {   // the mirror image
+                r = q;
+                c = p;
+            }
+            y = c < 16 ? 0 : r < 16 ? 1 : 2;
+            r &= 15u;
+            c &= 15u;
+        }
+        double sum = 0.0;
+#pragma unroll
+        for (uint32_t w = 0; w < 4; ++w) {
+            sum += part[((y * 4 + w) * 16 + r) * 16 + c];
+            if (kK == 8) sum += part[((y * 4 + w) * 16 + r + 8) * 16 + c + 8];
+        }
+        out[p * k + q] = sum;
     }
 }
 
@@ -961,71 +997,66 @@ struct SmallArgs {
     double coef[3 * kNsMaxSteps];
 };
 
-// One workgroup per matrix, kB x kB elements of every k x k matrix per thread.
-template <int kK, int kB>
-__global__ void __launch_bounds__(kK * kK / (kB * kB)) ns_small_iterate_kernel(const SmallArgs args)
+// One workgroup per matrix.  kK = 8: a thread per element.  kK = 16 and 32: a
+// wave per 16 x 16 tile, FP64 matrix instructions (32 x 32: 26 against ITERUS us
+// with two by two elements per thread).
+template <int kK>
+__global__ void __launch_bounds__(kK == 32 ? 256 : 64) ns_small_iterate_kernel(const SmallArgs args)
 {
-    constexpr int kSide = kK / kB;
+    constexpr int kE = kK == 8 ? 1 : 4;   // elements per thread
     __shared__ double s[kK][kK + 1], t[kK][kK + 1], p[kK][kK + 1], q[kK][kK + 1];
     const NsMat m = load_mat(args.tab, blockIdx.x);
     const uint32_t k = m.rows < m.cols ? m.rows : m.cols, l = m.rows < m.cols ? m.cols : m.rows;
     const uint32_t chunks = (l + kNsSmallChunk - 1) / kNsSmallChunk;
-    const uint32_t i = threadIdx.x / kSide, j = threadIdx.x % kSide;   // and i + kSide, ...
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+    // element e of a thread: row i + e * 4, column j
+    const uint32_t i = kK == 8 ? lane >> 3 : (wave >> 1) * 16 + (lane >> 4), j = kK == 8 ? lane & 7u : (wave & 1u) * 16 + (lane & 15u);
     const double* part = reinterpret_cast<const double*>(m.work);
-    double v[kB][kB];
+    double v[kE];
 #pragma unroll
-    for (int x = 0; x < kB; ++x)
-#pragma unroll
-        for (int y = 0; y < kB; ++y) {
-            const uint32_t ii = i + x * kSide, jj = j + y * kSide;
-            double sum = 0.0;
-            if (ii < k && jj < k) {
-                const double* from = part + ii * k + jj;
+    for (int e = 0; e < kE; ++e) {
+        const uint32_t ii = i + e * 4;
+        double sum = 0.0;
+        if (ii < k && j < k) {
+            const double* from = part + ii * k + j;
 #pragma unroll 8
-                for (uint32_t c = 0; c < chunks; ++c) sum += from[static_cast<uint64_t>(c) * k * k];
-            }
-            v[x][y] = sum;
-            s[ii][jj] = sum;
+            for (uint32_t c = 0; c < chunks; ++c) sum += from[static_cast<uint64_t>(c) * k * k];
         }
+        v[e] = sum;
+        s[ii][j] = sum;
+    }
     __syncthreads();
     double trace = 0.0;
 #pragma unroll
     for (int x = 0; x < kK; ++x) trace += s[x][x];   // zeros from k on
     const double inv = 1.0 / (sqrt(trace) + args.eps);
     __syncthreads();
-    auto put = [&](double (&to)[kK][kK + 1], const double (&from)[kB][kB]) {
+    auto put = [&](double (&to)[kK][kK + 1], const double (&from)[kE]) {
 #pragma unroll
-        for (int x = 0; x < kB; ++x)
-#pragma unroll
-            for (int y = 0; y < kB; ++y) to[i + x * kSide][j + y * kSide] = from[x][y];
+        for (int e = 0; e < kE; ++e) to[i + e * 4][j] = from[e];
     };
-    auto product = [&](const double (&a)[kK][kK + 1], const double (&b)[kK][kK + 1], double (&out)[kB][kB]) {
+    auto product = [&](const double (&a)[kK][kK + 1], const double (&b)[kK][kK + 1], double (&out)[kE]) {
+        if constexpr (kK == 8) {
+            double sum = 0.0;
 #pragma unroll
-        for (int x = 0; x < kB; ++x)
+            for (int e = 0; e < kK; ++e) sum = fma(a[i][e], b[e][j], sum);
+            out[0] = sum;
+        } else {
+            f64x4 sum = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-            for (int y = 0; y < kB; ++y) out[x][y] = 0.0;
-#pragma unroll 8
-        for (int e = 0; e < kK; ++e) {
-            double ax[kB], by[kB];
+            for (uint32_t e = 0; e < kK; e += 4)
+                sum = __builtin_amdgcn_mfma_f64_16x16x4f64(a[(wave >> 1) * 16 + (lane & 15u)][e + (lane >> 4)],
+                                                           b[e + (lane >> 4)][j], sum, 0, 0, 0);
 #pragma unroll
-            for (int x = 0; x < kB; ++x) {
-                ax[x] = a[i + x * kSide][e];
-                by[x] = b[e][j + x * kSide];
-            }
-#pragma unroll
-            for (int x = 0; x < kB; ++x)
-#pragma unroll
-                for (int y = 0; y < kB; ++y) out[x][y] = fma(ax[x], by[y], out[x][y]);
+            for (int e = 0; e < kE; ++e) out[e] = sum[e];
         }
     };
-    double w[kB][kB];
+    double w[kE];
 #pragma unroll
-    for (int x = 0; x < kB; ++x)
-#pragma unroll
-        for (int y = 0; y < kB; ++y) {
-            v[x][y] = v[x][y] * inv * inv;
-            w[x][y] = i + x * kSide == j + y * kSide ? inv : 0.0;   // Q_0 carries the scaling of u to X_0
-        }
+    for (int e = 0; e < kE; ++e) {
+        v[e] = v[e] * inv * inv;
+        w[e] = i + e * 4 == j ? inv : 0.0;   // Q_0 carries the scaling of u to X_0
+    }
     put(s, v);
     put(q, w);
     __syncthreads();
@@ -1033,10 +1064,7 @@ __global__ void __launch_bounds__(kK * kK / (kB * kB)) ns_small_iterate_kernel(c
         const double a = args.coef[3 * n], b = args.coef[3 * n + 1], c = args.coef[3 * n + 2];
         product(s, s, w);
 #pragma unroll
-        for (int x = 0; x < kB; ++x)
-#pragma unroll
-            for (int y = 0; y < kB; ++y)
-                w[x][y] = (i + x * kSide == j + y * kSide ? a : 0.0) + b * s[i + x * kSide][j + y * kSide] + c * w[x][y];
+        for (int e = 0; e < kE; ++e) w[e] = (i + e * 4 == j ? a : 0.0) + b * s[i + e * 4][j] + c * w[e];
         put(p, w);
         __syncthreads();
         product(p, s, w);
@@ -1050,24 +1078,21 @@ __global__ void __launch_bounds__(kK * kK / (kB * kB)) ns_small_iterate_kernel(c
     }
     double* out = reinterpret_cast<double*>(m.work) + static_cast<uint64_t>(chunks) * k * k;
 #pragma unroll
-    for (int x = 0; x < kB; ++x)
-#pragma unroll
-        for (int y = 0; y < kB; ++y) {
-            const uint32_t ii = i + x * kSide, jj = j + y * kSide;
-            if (ii < k && jj < k) out[ii * k + jj] = q[ii][jj];
-        }
+    for (int e = 0; e < kE; ++e) out[(i + e * 4) * kK + j] = q[i + e * 4][j];   // zeros from k on
 }
 
 template <int kK>
-__global__ void __launch_bounds__(256) ns_small_apply_kernel(const NsMat* tab, uint32_t n)
+__global__ void __launch_bounds__(256) ns_small_apply_kernel(const NsMat* tab, uint32_t n, NsIndex index)
 {
     __shared__ float u[kK * kSmallPitch];
-    __shared__ double q[kK * kK];
-    const NsMat m = load_mat(tab, find_mat<&NsMat::prep0>(tab, n, blockIdx.x));
+    const NsMat m = load_mat(tab, find_mat<&NsMat::prep0>(tab, n, index, blockIdx.x));
     const uint32_t l0 = (blockIdx.x - m.prep0) * kNsSmallChunk;
     const uint32_t k = m.rows < m.cols ? m.rows : m.cols, l = m.rows < m.cols ? m.cols : m.rows;
     const uint32_t chunks = (l + kNsSmallChunk - 1) / kNsSmallChunk;
     const bool tall = (m.flags & kNsTall) != 0;
+    __shared__ double q[kK * kK];
+    const double* src = reinterpret_cast<const double*>(m.work) + static_cast<uint64_t>(chunks) * k * k;
+    for (uint32_t v = threadIdx.x; v < kK * kK; v += 256) q[v] = src[v];
     constexpr int kQuads = kK / 4;
     f32x4 old[kQuads];
 #pragma unroll
@@ -1077,11 +1102,6 @@ __global__ void __launch_bounds__(256) ns_small_apply_kernel(const NsMat* tab, u
         old[x] = old_master4(m, r, c);
     }
     stage_u<kK, false>(m, l0, u);
-    const double* src = reinterpret_cast<const double*>(m.work) + static_cast<uint64_t>(chunks) * k * k;
-    for (uint32_t v = threadIdx.x; v < kK * kK; v += 256) {
-        const uint32_t i = v / kK, j = v % kK;
-        q[v] = i < k && j < k ? src[i * k + j] : 0.0;
-    }
     __syncthreads();
     // one column of u per thread, four rows of the result at a time
     float col[kK];
@@ -1111,17 +1131,16 @@ __global__ void __launch_bounds__(256) ns_small_apply_kernel(const NsMat* tab, u
 }
 
 template <int kK>
-hipError_t launch_small(const NsCall& c, const NsMat* tab, uint32_t n, uint32_t chunks, hipStream_t s)
+hipError_t launch_small(const NsCall& c, const NsMat* tab, uint32_t n, uint32_t chunks, const NsIndex& index, hipStream_t s)
 {
     SmallArgs args{};
     args.tab = tab;
     args.steps = c.steps;
     args.eps = c.eps;
     for (uint32_t k = 0; k < 3 * c.steps; ++k) args.coef[k] = c.coef[k];
-    hipLaunchKernelGGL(ns_small_gram_kernel<kK>, dim3(chunks), dim3(256), 0, s, tab, n);
-    constexpr int kB = kK == 32 ? 2 : 1;
-    hipLaunchKernelGGL((ns_small_iterate_kernel<kK, kB>), dim3(n), dim3(kK * kK / (kB * kB)), 0, s, args);
-    hipLaunchKernelGGL(ns_small_apply_kernel<kK>, dim3(chunks), dim3(256), 0, s, tab, n);
+    hipLaunchKernelGGL(ns_small_gram_kernel<kK>, dim3(chunks), dim3(256), 0, s, tab, n, index);
+    hipLaunchKernelGGL(ns_small_iterate_kernel<kK>, dim3(n), dim3(kK == 32 ? 256 : 64), 0, s, args);
+    hipLaunchKernelGGL(ns_small_apply_kernel<kK>, dim3(chunks), dim3(256), 0, s, tab, n, index);
     return hipGetLastError();
 }
 
@@ -1141,10 +1160,10 @@ public:
     hipError_t run()
     {
         const NsMat* tab = args_.tab;
-        hipLaunchKernelGGL(ns_norm_kernel, dim3(c_.prep_tiles), dim3(256), 0, s_, tab, c_.nbig, c_.layout, c_.counters, c_.ncounters);
+        hipLaunchKernelGGL(ns_norm_kernel, dim3(c_.prep_tiles), dim3(256), 0, s_, tab, c_.nbig, c_.prep_index, c_.layout, c_.counters, c_.ncounters);
         hipLaunchKernelGGL(ns_scale_kernel, dim3(c_.nbig), dim3(1024), 0, s_, tab, c_.layout, c_.eps);
-        if (xt_terms(0) == 2) hipLaunchKernelGGL((ns_split_kernel<kT, kTerms, 2>), dim3(c_.prep_tiles), dim3(256), 0, s_, tab, c_.nbig, c_.layout);
-        else hipLaunchKernelGGL((ns_split_kernel<kT, kTerms, 1>), dim3(c_.prep_tiles), dim3(256), 0, s_, tab, c_.nbig, c_.layout);
+        if (xt_terms(0) == 2) hipLaunchKernelGGL((ns_split_kernel<kT, kTerms, 2>), dim3(c_.prep_tiles), dim3(256), 0, s_, tab, c_.nbig, c_.prep_index, c_.layout);
+        else hipLaunchKernelGGL((ns_split_kernel<kT, kTerms, 1>), dim3(c_.prep_tiles), dim3(256), 0, s_, tab, c_.nbig, c_.prep_index, c_.layout);
         for (uint32_t k = 0; k < c_.steps;) {
             const bool pair = paired(k);
             gram();
@@ -1173,6 +1192,7 @@ private:
     void launch(const NsProduct& p)
     {
         args_.depth = p.depth;
+        args_.index = p.index;
         hipLaunchKernelGGL((ns_product_kernel<kT, kA, kB, kKind, kOut>), dim3(p.units), dim3(kT == 256 ? 512 : 256), 0, s_, args_);
     }
 
@@ -1261,9 +1281,9 @@ int ns_launch(const NsCall& c, NsMat* device_table, void* stream)
     const NsMat* tab = device_table;
     for (int k = 0; k < kNsClasses && err == hipSuccess; ++k) {
         if (c.nsmall[k] == 0) continue;
-        err = k == 0 ? launch_small<8>(c, tab, c.nsmall[k], c.small_chunks[k], s)
-            : k == 1 ? launch_small<16>(c, tab, c.nsmall[k], c.small_chunks[k], s)
-                     : launch_small<32>(c, tab, c.nsmall[k], c.small_chunks[k], s);
+        err = k == 0 ? launch_small<8>(c, tab, c.nsmall[k], c.small_chunks[k], c.small_index[k], s)
+            : k == 1 ? launch_small<16>(c, tab, c.nsmall[k], c.small_chunks[k], c.small_index[k], s)
+                     : launch_small<32>(c, tab, c.nsmall[k], c.small_chunks[k], c.small_index[k], s);
         tab += c.nsmall[k];
     }
     if (err == hipSuccess && c.nbig > 0) {

@@ -174,6 +174,66 @@ def test_orthogonalize_steps_eps_and_coefficients():
             assert err <= 4 * tolerance(r, c, True, False), (kw, r, c, err)
 
 
+def ortho64_gpu(x, steps=5, coef=COEF):
+    x = x.double()
+    if x.shape[0] > x.shape[1]:
+        return ortho64_gpu(x.T.contiguous(), steps, coef).T
+    x = x / (x.norm() + 1e-7)
+    for a, b, c in np.broadcast_to(np.asarray(coef, np.float64), (steps, 3)):
+        s = x @ x.T.contiguous()
+        x = float(a) * x + (float(b) * s + float(c) * (s @ s)) @ x
+    return x
+
+
+@pytest.mark.parametrize("shapes", [
+    [(300, 9001), (70, 4000)],          # long: steps in pairs, tiles of 64
+    [(2050, 2311)],                     # nearly square: single steps, tiles of 128
+    [(777, 9000), (9001, 1030)],        # steps in pairs, tiles of 128
+    [(4099, 4501)],                     # tiles of 256, single steps
+    [(12001, 3001)],                    # tiles of 256, steps in pairs
+])
+@pytest.mark.parametrize("precision", [lso.LSO_NS_FULL, lso.LSO_NS_HALF])
+def test_orthogonalize_large(shapes, precision):
+    T = torch()
+    T.manual_seed(5)
+    xs = [T.randn(r, c, device="cuda") + 3.0 * T.outer(T.randn(r, device="cuda"), T.randn(c, device="cuda")) for r, c in shapes]
+    ys = [T.full_like(x, 7.0) for x in xs]
+    table = lso.MatrixTable.from_rows(dict(x=x, y=y, rows=x.shape[0], cols=x.shape[1]) for x, y in zip(xs, ys))
+    need = lso.orthogonalize_workspace_bytes(table, precision)
+    ws = workspace(need)
+    for steps in (5, 1, 4):
+        log(f"orthogonalize large {shapes} precision {precision} steps {steps}")
+        lso.orthogonalize(table, ws, need, steps=steps, precision=precision)
+        T.cuda.synchronize()
+        assert bool((ws[need:] == CANARY).all())
+        for x, y in zip(xs, ys):
+            want = ortho64_gpu(x, steps)
+            err = float((y.double() - want).norm() / want.norm())
+            assert err <= tolerance(*x.shape, precision == lso.LSO_NS_FULL, False), (x.shape, steps, err)
+            share = tolerance(*x.shape, precision == lso.LSO_NS_FULL, False) * float(want.norm()) / math.sqrt(want.numel())
+            assert float((y.double() - want).abs().max()) <= 12 * share
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 6])
+@pytest.mark.parametrize("precision", [lso.LSO_NS_FULL, lso.LSO_NS_HALF])
+def test_orthogonalize_steps_in_pairs(steps, precision):
+    """Every way that a number of steps is taken in pairs and singly, with
+    coefficients that allow pairs everywhere, nowhere and in places (a pair is
+    taken where the product of its two polynomials stays in FP16's range)."""
+    shapes = [(50, 3000), (3000, 90)]
+    mild, steep = (1.5, -0.5, 0.0), (8.0, -20.0, 13.0)   # 1.5 x 8 < 15.9 < 8 x 8
+    for coef in ([mild] * steps, [steep] + [mild] * (steps - 1), [mild if k % 3 else steep for k in range(steps)]):
+        m = Mats(shapes, seed=60 + steps)
+        log(f"orthogonalize in pairs: {steps} steps, precision {precision}, {coef}")
+        for (r, c), src, got in zip(shapes, m.src, run_ortho(m, steps=steps, coefficients=coef, precision=precision)):
+            want = ortho64(src, steps, coef=coef)
+            # steep steps: Lipschitz constant 8 where the default's is 3.9, and (8 + 3 20 s^2 + 5 13 s^4) / 46 < 3 times
+            # its rounding, for at most two of six steps
+            allow = 3 * (8 / 3.9)**2 * tolerance(r, c, precision == lso.LSO_NS_FULL, False)
+            err = np.linalg.norm(got - want) / np.linalg.norm(want)
+            assert err <= allow, (r, c, coef, err, allow)
+
+
 def test_orthogonalize_extreme_values():
     """Zero matrices, one element, tiny and huge scales (|u|_F is summed in
     FP64), and a NaN or an infinity that stays in its own matrix."""
