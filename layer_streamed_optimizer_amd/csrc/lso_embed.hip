@@ -432,6 +432,16 @@ __device__ __forceinline__ void grad_rows(const GradArgs& a, uint32_t v0, uint32
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t v1 = a.vocab - v0 < rows ? a.vocab : v0 + rows;
     uint32_t first = uniform(find_run(a.keys, a.n, v0));
+    if (first >= a.n || uniform(a.keys[first]) >= v1) {
+        // no token here: most waves of a short batch
+        if (a.add) return;
+        float zero[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) zero[e] = 0.0f;
+        for (uint32_t v = v0; v < v1; ++v)
+            for (uint32_t c = lane * V; c < a.width; c += 64 * V) store_values<V, kTableF32, false>(a.table, v * a.ld_table + c, zero);
+        return;
+    }
     for (uint32_t v = v0; v < v1; ++v) {
         const uint64_t at = static_cast<uint64_t>(first) + lane;
         const uint32_t key = at < a.n ? a.keys[at] : 0xFFFFFFFFu;
@@ -582,7 +592,8 @@ Tokens tokens_of(const lso_embed& e)
     return {e.tokens, static_cast<uint32_t>(e.n), static_cast<uint32_t>(e.vocab), e.token_dtype == LSO_DT_I64};
 }
 
-// Table rows per wave of the gradient: several where most rows are empty.
+// Table rows per wave of the gradient: several where most rows are empty
+// (257 tokens, 32000 rows: 1 row 33.6, 2 rows 30.6, 4 rows 30.0, 8 rows 34.8 us).
 uint32_t rows_of_wave(uint64_t n, uint64_t vocab) { return n * 4 <= vocab ? 4 : 1; }
 
 bool beyond_l2(const lso_embed& e) { return e.n * e.width * elem_bytes(e.rows_dtype) > kL2Bytes; }

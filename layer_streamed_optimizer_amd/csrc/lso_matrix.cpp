@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "lso_ns.h"
@@ -13,7 +14,7 @@ namespace lso {
 namespace {
 
 constexpr uint64_t kMaxSide = (1ull << 31) - 1;
-constexpr uint64_t kMaxIndex = (1ull << 24) - 8;   // workgroups of a launch: 256 lanes each, under 2^32 in all
+constexpr uint64_t kMaxIndex = (1ull << 23) - 8;   // workgroups of a launch: up to 512 lanes each, under 2^32 in all
 constexpr double kDefaultCoef[3] = {3.4445, -4.7750, 2.0315};
 
 // A matrix of either call, before its place in the plan.
@@ -109,8 +110,28 @@ lso_status take_array(std::vector<Interval>& iv, uintptr_t addr, uint64_t bytes,
     return LSO_OK;
 }
 
-// The checks of lso_orthogonalize; with iv, of its addresses too.
-lso_status collect(const lso_matrix* mats, size_t n, std::vector<Item>& items, std::vector<Interval>* iv, bool& all_bf16)
+// The arrays of a call by kind: those of a kind mostly lie in order, so their
+// check sorts little.
+struct Arrays {
+    std::vector<Interval> kind[4];
+
+    std::vector<Interval> all()
+    {
+        std::vector<Interval> iv;
+        iv.reserve(kind[0].size() + kind[1].size() + kind[2].size() + kind[3].size() + 1);
+        for (const auto& k : kind) {
+            const size_t at = iv.size();
+            iv.insert(iv.end(), k.begin(), k.end());
+            const auto below = [](const Interval& a, const Interval& b) { return a.lo < b.lo; };
+            if (!std::is_sorted(iv.begin() + at, iv.end(), below)) std::sort(iv.begin() + at, iv.end(), below);
+            std::inplace_merge(iv.begin(), iv.begin() + at, iv.end(), below);
+        }
+        return iv;
+    }
+};
+
+// The checks of lso_orthogonalize; with arrays, of its addresses too.
+lso_status collect(const lso_matrix* mats, size_t n, std::vector<Item>& items, Arrays* arrays, bool& all_bf16)
 {
     if (n > 0 && !mats) return fail(LSO_E_INVALID, "mats is NULL");
     all_bf16 = true;
@@ -126,13 +147,13 @@ lso_status collect(const lso_matrix* mats, size_t n, std::vector<Item>& items, s
             return fail(LSO_E_INVALID, "matrix %zu: a row stride is smaller than cols, or too large", i);
         if (a.y_dtype != LSO_DT_BF16) all_bf16 = false;
         const uint64_t ex = a.x_dtype == LSO_DT_F32 ? 4 : 2, ey = a.y_dtype == LSO_DT_F32 ? 4 : 2;
-        if (iv) {
+        if (arrays) {
             const bool same = a.x == a.y && a.x_dtype == a.y_dtype && a.ld_x == a.ld_y;
             if (!same) {
-                s = take_array(*iv, reinterpret_cast<uintptr_t>(a.x), span(a.rows, a.cols, a.ld_x, ex), ex, false, i, "x");
+                s = take_array(arrays->kind[0], reinterpret_cast<uintptr_t>(a.x), span(a.rows, a.cols, a.ld_x, ex), ex, false, i, "x");
                 if (s != LSO_OK) return s;
             }
-            s = take_array(*iv, reinterpret_cast<uintptr_t>(a.y), span(a.rows, a.cols, a.ld_y, ey), ey, true, i, "y");
+            s = take_array(arrays->kind[1], reinterpret_cast<uintptr_t>(a.y), span(a.rows, a.cols, a.ld_y, ey), ey, true, i, "y");
             if (s != LSO_OK) return s;
         }
         Item it{};
@@ -149,7 +170,7 @@ lso_status collect(const lso_matrix* mats, size_t n, std::vector<Item>& items, s
     return LSO_OK;
 }
 
-lso_status collect(const lso_muon_block* blocks, size_t n, std::vector<Item>& items, std::vector<Interval>* iv, bool& all_bf16)
+lso_status collect(const lso_muon_block* blocks, size_t n, std::vector<Item>& items, Arrays* arrays, bool& all_bf16)
 {
     if (n > 0 && !blocks) return fail(LSO_E_INVALID, "blocks is NULL");
     all_bf16 = false;   // the result is the FP32 master
@@ -170,16 +191,17 @@ lso_status collect(const lso_muon_block* blocks, size_t n, std::vector<Item>& it
         const uintptr_t base = reinterpret_cast<uintptr_t>(b.base);
         const uint64_t count = b.rows * b.cols, eg = b.grad_dtype == LSO_DT_F32 ? 4 : 2;
         const bool weight = b.weight_dtype == LSO_DT_BF16;
-        if (iv) {
+        if (arrays) {
             const struct { uint64_t off, elem; bool used, written; const char* name; } arr[4] = {
                 {b.off_master, 4, true, true, "master"},
                 {b.off_m, 4, true, true, "m"},
                 {b.off_grad, eg, true, false, "grad"},
                 {b.off_weight, 2, weight, true, "weight"},
             };
-            for (const auto& a : arr) {
+            for (size_t k = 0; k < 4; ++k) {
+                const auto& a = arr[k];
                 if (!a.used) continue;
-                s = take_array(*iv, base + a.off, count * a.elem, a.elem, a.written, i, a.name);
+                s = take_array(arrays->kind[k], base + a.off, count * a.elem, a.elem, a.written, i, a.name);
                 if (s != LSO_OK) return s;
             }
         }
@@ -316,9 +338,17 @@ uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<N
     table.clear();
     table.reserve(items.size());
     // a launch ends sooner if the longest units start first
-    std::stable_sort(items.begin(), items.end(), [](const Item& a, const Item& b) {
-        return std::max(a.rows, a.cols) > std::max(b.rows, b.cols);
-    });
+    const auto longer = [](const Item& a, const Item& b) { return std::max(a.rows, a.cols) > std::max(b.rows, b.cols); };
+    if (!std::is_sorted(items.begin(), items.end(), longer)) {
+        std::vector<std::pair<uint64_t, uint32_t>> order;   // longest first, then as given
+        order.reserve(items.size());
+        for (uint32_t i = 0; i < items.size(); ++i) order.push_back({UINT64_MAX - std::max(items[i].rows, items[i].cols), i});
+        std::sort(order.begin(), order.end());
+        std::vector<Item> sorted;
+        sorted.reserve(items.size());
+        for (const auto& o : order) sorted.push_back(items[o.second]);
+        items.swap(sorted);
+    }
     c.tile = tile_edge(items);
     const uint64_t edge = c.tile;
     std::vector<Tiles> lists[4];
@@ -361,7 +391,7 @@ uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<N
                 lists[3].push_back({tm * tn, mp / 32});
             }
             ++count;
-            most_index = std::max({most_index, chunks, prep, uint64_t{count} * 4});
+            most_index = std::max({most_index, chunks, prep, uint64_t{count} * 2});
             table.push_back(m);
         }
         if (cls < kNsClasses) {
@@ -436,10 +466,11 @@ lso_status run(const T* list, size_t n, const lso_ns_params* params, void* works
     NsCall c{};
     std::vector<Item> items;
     std::vector<NsMat> table;
-    std::vector<Interval> iv;
+    Arrays arrays;
     bool all_bf16;
+    items.reserve(n < 65536 ? n : 65536);
     lso_status s = check_params(params, c);
-    if (s == LSO_OK) s = collect(list, n, items, &iv, all_bf16);
+    if (s == LSO_OK) s = collect(list, n, items, &arrays, all_bf16);
     if (s != LSO_OK) return s;
     if (items.empty()) return LSO_OK;
     c.layout = layout_of(params, all_bf16, items, c);
@@ -450,6 +481,7 @@ lso_status run(const T* list, size_t n, const lso_ns_params* params, void* works
     if (bytes < need)
         return fail(LSO_E_INVALID, "workspace of %llu bytes is smaller than the %llu this call needs",
                     static_cast<unsigned long long>(bytes), static_cast<unsigned long long>(need));
+    std::vector<Interval> iv = arrays.all();
     if (!add_array(iv, reinterpret_cast<uintptr_t>(workspace), need, true, n))
         return fail(LSO_E_INVALID, "workspace range wraps the address space");
     s = check_overlap(iv);

@@ -71,7 +71,15 @@ uint64_t tiled_bytes(uint64_t n)
 
 lso_status check_overlap(std::vector<Interval>& iv)
 {
-    std::sort(iv.begin(), iv.end(), [](const Interval& a, const Interval& b) { return a.lo < b.lo; });
+    const auto below = [](const Interval& a, const Interval& b) { return a.lo < b.lo; };
+    if (!iv.empty() && std::is_sorted(iv.begin(), iv.end() - 1, below)) {
+        // in order but for the last (a workspace): put that where it belongs
+        const Interval last = iv.back();
+        iv.pop_back();
+        iv.insert(std::upper_bound(iv.begin(), iv.end(), last, below), last);
+    } else {
+        std::sort(iv.begin(), iv.end(), below);
+    }
     uintptr_t end_all = 0, end_written = 0;
     size_t blk_all = 0, blk_written = 0;
     for (const Interval& x : iv) {

@@ -49,10 +49,9 @@ class _Table:
 
     @classmethod
     def from_rows(cls, rows: Iterable[dict]):
-        rows = list(rows)
-        tab = cls(len(rows))
-        for i, r in enumerate(rows):
-            tab.set_row(i, **r)
+        fields = [cls._fields(**r) for r in rows]
+        tab = cls(len(fields))
+        tab.arr[:] = fields
         return tab
 
     @property
@@ -65,16 +64,15 @@ class MatrixTable(_Table):
 
     DTYPE = MATRIX_DTYPE
 
-    def set_row(self, i: int, *, x, y, rows: int, cols: int, ld_x: int | None = None, ld_y: int | None = None,
-                x_dtype: int = LSO_DT_F32, y_dtype: int = LSO_DT_F32) -> None:
-        """x and y are torch tensors (their data_ptr) or device addresses;
-        strides default to cols."""
-        row = self.arr[i]
-        row["x"], row["y"] = _addr(x), _addr(y)
-        row["rows"], row["cols"] = rows, cols
-        row["ld_x"] = cols if ld_x is None else ld_x
-        row["ld_y"] = cols if ld_y is None else ld_y
-        row["x_dtype"], row["y_dtype"] = x_dtype, y_dtype
+    @staticmethod
+    def _fields(*, x, y, rows: int, cols: int, ld_x: int | None = None, ld_y: int | None = None, x_dtype: int = LSO_DT_F32,
+                y_dtype: int = LSO_DT_F32) -> tuple:
+        return (_addr(x), _addr(y), rows, cols, cols if ld_x is None else ld_x, cols if ld_y is None else ld_y, x_dtype, y_dtype)
+
+    def set_row(self, i: int, **row) -> None:
+        """x, y (torch tensors, by their data_ptr, or device addresses), rows,
+        cols, ld_x, ld_y (default cols), x_dtype, y_dtype (default FP32)."""
+        self.arr[i] = self._fields(**row)
 
 
 class MuonTable(_Table):
@@ -83,20 +81,18 @@ class MuonTable(_Table):
 
     DTYPE = MUON_DTYPE
 
-    def set_row(self, i: int, *, rows: int, cols: int, master, m, grad, weight=None, base: int = 0,
-                grad_dtype: int = LSO_DT_BF16, nesterov: bool = True, lr: float = 1e-3, beta: float = 0.95,
-                weight_decay: float = 0.0, scale: float = 1.0) -> None:
-        """Arrays are torch tensors or integer device addresses (offsets from
-        base if base != 0)."""
-        row = self.arr[i]
-        row["base"] = base
-        row["rows"], row["cols"] = rows, cols
-        row["off_master"], row["off_m"], row["off_grad"] = _addr(master), _addr(m), _addr(grad)
-        row["off_weight"] = _addr(weight)
-        row["grad_dtype"] = grad_dtype
-        row["weight_dtype"] = LSO_DT_BF16 if weight is not None else LSO_DT_NONE
-        row["flags"] = LSO_MUON_NESTEROV if nesterov else 0
-        row["lr"], row["beta"], row["weight_decay"], row["scale"] = lr, beta, weight_decay, scale
+    @staticmethod
+    def _fields(*, rows: int, cols: int, master, m, grad, weight=None, base: int = 0, grad_dtype: int = LSO_DT_BF16,
+                nesterov: bool = True, lr: float = 1e-3, beta: float = 0.95, weight_decay: float = 0.0, scale: float = 1.0) -> tuple:
+        return (base, rows, cols, _addr(master), _addr(m), _addr(grad), _addr(weight), grad_dtype,
+                LSO_DT_BF16 if weight is not None else LSO_DT_NONE, LSO_MUON_NESTEROV if nesterov else 0, 0, lr, beta, weight_decay,
+                scale)
+
+    def set_row(self, i: int, **row) -> None:
+        """rows, cols; master, m, grad and weight (or None): torch tensors or
+        device addresses (offsets from base if base != 0); grad_dtype,
+        nesterov, lr, beta, weight_decay, scale."""
+        self.arr[i] = self._fields(**row)
 
     def set_lr(self, lr: float) -> None:
         self.arr["lr"] = lr
