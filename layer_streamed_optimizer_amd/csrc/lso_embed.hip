@@ -36,14 +36,14 @@ constexpr uint32_t kMinSortTile = 512;
 constexpr uint32_t kRankSort = 4096;     // up to so many tokens are sorted by counting
 constexpr uint64_t kMaxGroups = (1ull << 24) - 1;   // workgroups of a launch: 256 lanes each, under 2^32 in all
 
-// Where the rows of a call exceed the eight XCDs' L2s (4 MB each), a lookup's
-// rows are stored past them, and a gradient's rows are read past them.
-// Measured: 16384 tokens of width 2048 looked up in 16.9 against 18.5 us; the
-// gradient of 32768 tokens of width 4096 in 151 against 177 us, of 131072 of
-// width 8192 in 815 against 860 us.  It costs where the rows are small (the
-// gradient of 257 tokens of width 2048 46 against 34 us), on the table's rows
-// that a lookup reads and tokens share (29.6 us), and on the gradient's table
-// (163 us).
+// What passes the caches (non-temporal).  Measured with outputs in turn, so
+// that none is still cached: the gradient's table always (257 tokens of width
+// 2048 33.0 against 40.5 us, 32768 of width 4096 161 against 168 us); where
+// the rows of a call exceed the eight XCDs' L2s (4 MB each), the rows that a
+// lookup writes (16384 tokens of width 2048 16.9 against 18.5 us) and a
+// gradient reads (131072 of width 8192 827 against 852 us; small ones lose: 257
+// tokens 46 against 34 us).  Not the table's rows that a lookup reads, which
+// tokens share (29.6 us).
 constexpr uint64_t kL2Bytes = 32ull << 20;
 
 // The sorted positions do not change while a gradient kernel runs, and a
@@ -383,7 +383,7 @@ __device__ __forceinline__ void put_gradient(const GradArgs& a, uint32_t v, uint
 #pragma unroll
         for (int e = 0; e < V; ++e) sum[e] += old[e];
     }
-    store_values<V, kTableF32, false>(a.table, i, sum);
+    store_values<V, kTableF32, true>(a.table, i, sum);
 }
 
 // The runs at the two ends of block b of kRun sorted positions.  first_*:
@@ -439,7 +439,7 @@ __device__ __forceinline__ void grad_rows(const GradArgs& a, uint32_t v0, uint32
 #pragma unroll
         for (int e = 0; e < V; ++e) zero[e] = 0.0f;
         for (uint32_t v = v0; v < v1; ++v)
-            for (uint32_t c = lane * V; c < a.width; c += 64 * V) store_values<V, kTableF32, false>(a.table, v * a.ld_table + c, zero);
+            for (uint32_t c = lane * V; c < a.width; c += 64 * V) store_values<V, kTableF32, true>(a.table, v * a.ld_table + c, zero);
         return;
     }
     for (uint32_t v = v0; v < v1; ++v) {
@@ -593,7 +593,8 @@ Tokens tokens_of(const lso_embed& e)
 }
 
 // Table rows per wave of the gradient: several where most rows are empty
-// (257 tokens, 32000 rows: 1 row 33.6, 2 rows 30.6, 4 rows 30.0, 8 rows 34.8 us).
+// (257 tokens, 32000 rows, cached: 1 row 33.6, 2 rows 30.6, 4 rows 30.0, 8 rows
+// 34.8 us).
 uint32_t rows_of_wave(uint64_t n, uint64_t vocab) { return n * 4 <= vocab ? 4 : 1; }
 
 bool beyond_l2(const lso_embed& e) { return e.n * e.width * elem_bytes(e.rows_dtype) > kL2Bytes; }
