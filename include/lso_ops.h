@@ -39,10 +39,13 @@ extern "C" {
  *   LSO_NS_FULL  operands of every product are held as a sum of two FP16
  *                numbers (22 significant bits), products are summed in FP32:
  *                results as accurate as FP32 products;
- *   LSO_NS_HALF  S, S^2 and the polynomial are rounded to FP16 (11 bits),
- *                X itself keeps 22: errors of about 1e-3 of |y|_F, below the
- *                rounding of a BF16 result, at less than half the time;
+ *   LSO_NS_HALF  what X is multiplied by is rounded to FP16 (11 bits), X
+ *                itself keeps 22 but for its last steps: errors of about
+ *                1e-3 of |y|_F, below the rounding of a BF16 result, at less
+ *                than half the time;
  *   LSO_NS_AUTO  HALF if every y of the call is BF16, else FULL.
+ * Two steps are taken as one product with X where that saves operations
+ * (S of the next step follows from the polynomial and S).
  * Matrices whose smaller side is at most LSO_NS_SMALL_SIDE take another way
  * whatever the precision: S is iterated on in FP64 and x multiplied once.
  * A matrix with a NaN or an infinity gives NaNs (in that matrix only); a
@@ -83,7 +86,8 @@ typedef struct lso_matrix {
 
 /* lso_orthogonalize: every matrix of the call, in a fixed number of launches
  * (the matrices advance together).  Workspace: at least
- * lso_orthogonalize_workspace_bytes (0 if the arguments are not valid).
+ * lso_orthogonalize_workspace_bytes (0 if the arguments are not valid), which
+ * depends on the sizes, the types and the precision.
  * Errors: INVALID, ALIGN, DTYPE, OVERLAP (nothing enqueued), HIP. */
 uint64_t   lso_orthogonalize_workspace_bytes(const lso_matrix* mats, size_t n, const lso_ns_params* params);
 lso_status lso_orthogonalize(const lso_matrix* mats, size_t n, const lso_ns_params* params, void* workspace,

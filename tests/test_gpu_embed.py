@@ -189,6 +189,28 @@ def test_gradient_ignores_what_padding_holds_and_repeats_bit_for_bit():
     assert np.isfinite(a.host()).all() and np.array_equal(a.host(), b.host())
 
 
+def test_two_gradients_at_once_on_two_streams():
+    T = torch()
+    n, vocab, width = 9000, 400, 512
+    rng = np.random.default_rng(6)
+    calls = []
+    for k in range(2):
+        t = tokens(n, vocab, 40 + k)
+        dy = Strided(n, width, "bf16", fill=rng.standard_normal((n, width)).astype(np.float32))
+        one, two = Strided(vocab, width, "f32"), Strided(vocab, width, "f32")
+        run_grad(t, dy, one)
+        need = lso.embed_grad_workspace_bytes(n, vocab, width)
+        calls.append((T.from_numpy(t).cuda(), dy, one, two, workspace(need), need, T.cuda.Stream()))
+    T.cuda.synchronize()
+    log("two gradients at once")
+    for _ in range(3):
+        for t, dy, _, two, ws, need, s in calls:
+            lso.embed_grad(t, dy.t, two.t, ws, need, stream=s)
+    T.cuda.synchronize()
+    for _, _, one, two, _, _, _ in calls:
+        assert T.equal(one.t, two.t)
+
+
 def test_wide_token_values_are_padding_not_wrapped():
     t = np.array([1, (1 << 32) + 1, -(1 << 32) + 1, (1 << 62), 2], np.int64)
     fill = np.arange(1, 41, dtype=np.float32).reshape(5, 8)

@@ -485,6 +485,64 @@ def test_many_matrices_in_one_call():
     b.check(what="many")
 
 
+def test_matrices_of_many_different_sizes():
+    """More different sizes than a launch's runs of alike matrices hold, of the
+    small and of the general path: workgroups then search the table."""
+    shapes = [(3, 270 * i + 5) for i in range(1, 13)] + [(40 + 30 * i, 50 + 70 * i) for i in range(12)]
+    for precision in (lso.LSO_NS_FULL, lso.LSO_NS_HALF):
+        m = Mats(shapes, seed=80)
+        log(f"orthogonalize {len(shapes)} different sizes, precision {precision}")
+        for (r, c), src, got in zip(shapes, m.src, run_ortho(m, precision=precision)):
+            check(got, ortho64(src), r, c, precision == lso.LSO_NS_FULL, False, f"{r}x{c}")
+
+
+def test_a_large_table_in_a_graph():
+    """As many adapters as a model has, captured: the table travels in the
+    arguments of a launch that the graph keeps."""
+    T = torch()
+    shapes = [(8, 64 + 8 * (i % 5)) for i in range(330)] + [(60, 8)] * 20
+    eager, graphed = Block(shapes, "f32", False, seed=90, lr=0.1), Block(shapes, "f32", False, seed=90, lr=0.1)
+    need = lso.muon_workspace_bytes(eager.table)
+    ws = [workspace(need), workspace(need)]
+    log("many adapters eager")
+    lso.muon_step(eager.table, ws[0], need)
+    T.cuda.synchronize()
+    eager.check(what="eager")
+    log("many adapters captured")
+    g = T.cuda.CUDAGraph()
+    with T.cuda.graph(g):
+        lso.muon_step(graphed.table, ws[1], need)
+    graphed.table.arr["rows"] = 0          # the host table is not read again
+    for k in range(3):
+        g.replay()
+        T.cuda.synchronize()
+        if k > 0:
+            lso.muon_step(eager.table, ws[0], need)
+            T.cuda.synchronize()
+        assert T.equal(eager.master, graphed.master) and T.equal(eager.m, graphed.m), f"replay {k}"
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Two calls with workspaces of their own on two streams at once give what
+    they give one after the other."""
+    T = torch()
+    shapes = [[(300, 2000), (8, 900)], [(500, 700), (16, 5000)]]
+    want = [run_ortho(Mats(s, seed=95 + i)) for i, s in enumerate(shapes)]
+    mats = [Mats(s, seed=95 + i) for i, s in enumerate(shapes)]
+    need = [lso.orthogonalize_workspace_bytes(m.table) for m in mats]
+    ws = [workspace(n) for n in need]
+    streams = [T.cuda.Stream(), T.cuda.Stream()]
+    T.cuda.synchronize()
+    log("two calls at once")
+    for _ in range(3):
+        for m, n, w, s in zip(mats, need, ws, streams):
+            lso.orthogonalize(m.table, w, n, stream=s)
+    T.cuda.synchronize()
+    for m, w in zip(mats, want):
+        for a, b in zip(m.results(), w):
+            assert np.array_equal(a, b)
+
+
 def test_errors_leave_the_thread_usable():
     lib = lso._native.lib()
     assert lib.lso_muon_step(None, 1, None, None, 0, None) == 1
