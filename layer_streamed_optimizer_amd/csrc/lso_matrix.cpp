@@ -234,6 +234,7 @@ lso_status collect(const lso_muon_block* blocks, size_t n, std::vector<Item>& it
 // the sums).
 struct Tiles {
     uint64_t count, stages;   // of one matrix in one launch
+    uint64_t matrices;        // so many with the same numbers
 };
 // kPartCost: measured over calls of one to four matrices of 64 x 2048 to 4096 x 4096:
 // 8 and 16 cut too finely (1024 x 1024 half precision 243 against 178 us with
@@ -243,42 +244,40 @@ constexpr uint64_t kPartCost = 64;
 uint64_t units_of(const std::vector<Tiles>& list, uint64_t depth)
 {
     uint64_t units = 0;
-    for (const Tiles& t : list) units += (t.count * ((t.stages + depth - 1) / depth) + 7) / 8 * 8;
+    for (const Tiles& t : list) units += t.matrices * ((t.count * ((t.stages + depth - 1) / depth) + 7) / 8 * 8);
     return units;
 }
 
-uint32_t part_depth(const std::vector<Tiles>& list, uint64_t slots)
+uint32_t part_depth(const std::vector<Tiles>& matrices, uint64_t slots)
 {
+    std::vector<Tiles> list;   // equal ones, which mostly lie in a row, together
     uint64_t most = 1;
-    for (const Tiles& t : list) most = std::max(most, t.stages);
+    for (const Tiles& t : matrices) {
+        most = std::max(most, t.stages);
+        if (!list.empty() && list.back().count == t.count && list.back().stages == t.stages) ++list.back().matrices;
+        else list.push_back(t);
+    }
     const uint64_t whole_units = units_of(list, most);
     if (whole_units > 8 * slots) return static_cast<uint32_t>(most);   // many rounds: nothing to gain
     uint64_t best = most, best_cost = (whole_units + slots - 1) / slots * (most + kPartCost / 2);
     for (uint64_t depth = most - 1; depth >= 8; --depth) {
-        const uint64_t units = units_of(list, depth), cost = (units + slots - 1) / slots * (depth + kPartCost);
+        const uint64_t units = units_of(list, depth);
+        if (units > 8 * slots) break;
+        // the smallest depth with as many parts of each matrix: as many units,
+        // and the cheapest (trying each depth took 11 ms for 40 x 2^26)
+        uint64_t same = 8;
+        for (const Tiles& t : list) {
+            const uint64_t parts = (t.stages + depth - 1) / depth;
+            same = std::max(same, (t.stages + parts - 1) / parts);
+        }
+        depth = std::min(depth, same);
+        const uint64_t cost = (units + slots - 1) / slots * (depth + kPartCost);
         if (cost < best_cost) {
             best = depth;
             best_cost = cost;
         }
-        if (units > 8 * slots) break;
     }
     return static_cast<uint32_t>(best);
-}
-
-// The edge of the products' tiles.  Large tiles load less per operation, small
-// ones fill the 256 CUs and the pipeline with less work.  By the operations
-// of a step; measured (us, edges 64 / 128 / 256): 22 of 256 x 2048 in half
-// precision (0.9e10) 290 / 369 / 470; in full precision 1024 x 4096 (1.4e10) 416 /
-// 535 / 1305, 2048 x 2048 (3.4e10) 725 / 700 / 1373, three of 2048 x 5632
-// (2.4e11) 4526 / 3693 / 3951, 4096 x 4096 (2.7e11) 4787 / 4092 / 3761.
-uint32_t tile_edge(const std::vector<Item>& items)
-{
-    double work = 0.0;
-    for (const Item& it : items) {
-        const uint64_t k = std::min(it.rows, it.cols), l = std::max(it.rows, it.cols);
-        if (small_class(k) < 0) work += static_cast<double>(k) * k * (3.0 * l + k);
-    }
-    return work >= 2.6e11 ? 256 : work >= 3e10 ? 128 : 64;
 }
 
 // The index of `count` matrices in a launch of `total` workgroups, by the first
@@ -301,7 +300,50 @@ NsIndex index_of(const NsMat* mats, uint32_t count, uint32_t NsMat::*first, uint
     return x;
 }
 
-// How the call's numbers are held, and whether steps are taken in pairs:
+// Whether to take steps in pairs, by the matrix-core products of two steps: a
+// pair has seven launches instead of six, so small calls need a larger saving.
+bool pairs_pay(uint32_t edge, double single, double pair) { return pair * (edge == 64 ? 1.4 : 1.1) < single; }
+
+// The edge of the products' tiles.  Large tiles load less per operation; small
+// ones fill the 256 CUs with less work, waste less on padding and on the upper
+// half of diagonal tiles, and fill and drain their pipeline sooner.  The edge
+// is the one whose launches of five steps cost least: a tile costs its stages
+// and `tile` more, a launch `launch` stages of latency, and `slots` workgroups
+// take `us` for a stage.  The numbers are fitted to 112 measured calls, one
+// to 1120 matrices of 33 x 4096 to 8192 x 8192 in both precisions, whose time is
+// 1.1% over the best edge's in the mean and 11% at most (a rule by the operations
+// of a step alone was 4.3% over and up to twice).  Measured (us, edges 64 / 128 /
+// 256): 22 of 256 x 2048 in half precision 301 / 383 / 600; in full precision
+// 1120 of 64 x 4096 6770 / 13778 / 43963, 2048 x 2048 850 / 777 / 1349, the seven of a
+// TinyLlama layer 5977 / 4003 / 4220, three of 4096 x 4096 15106 / 11164 / 10441.
+uint32_t tile_edge(const std::vector<Item>& items, double single, double pair)
+{
+    constexpr struct { uint32_t edge; double slots, tile, launch, us; } edges[3] = {
+        {64, 1024, 32, 24, 0.29}, {128, 512, 80, 80, 0.286}, {256, 256, 128, 160, 0.4}};
+    uint32_t best = 64;
+    double best_cost = INFINITY;
+    for (const auto& x : edges) {
+        // launches with S, with the other squares and with X
+        const bool pairs = pairs_pay(x.edge, single, pair);
+        const double grams = pairs ? 3 : 5, squares = pairs ? 11 : 5, applies = pairs ? 3 : 5;
+        double stages = 0.0;
+        for (const Item& it : items) {
+            const uint64_t k = std::min(it.rows, it.cols), l = std::max(it.rows, it.cols);
+            if (small_class(k) >= 0) continue;
+            const double tm = static_cast<double>((k + x.edge - 1) / x.edge), tn = static_cast<double>((l + x.edge - 1) / x.edge);
+            const double half = tm * (tm + 1) / 2, m = tm * x.edge / 16 + x.tile, n = tn * x.edge / 16 + x.tile;
+            stages += grams * half * n + squares * half * m + applies * tm * tn * m;
+        }
+        const double cost = x.us * (stages / x.slots + (grams + squares + applies) * x.launch);
+        if (cost < best_cost) {
+            best = x.edge;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
+// How the call's numbers are held, its tiles' edge, and whether steps are taken in pairs:
 // X_{k+2} = Q X_k with Q = P' P, P' the polynomial in S' = P S P.  A step by
 // itself makes S = X X^T (half of it, m^2 n operations), S^2 (m^3) and P X (2 m^2 n); a
 // pair makes S, Q X and five products of m x m, so it saves 3 m^2 n - 3 m^3
@@ -311,7 +353,7 @@ NsIndex index_of(const NsMat* mats, uint32_t count, uint32_t NsMat::*first, uint
 // below that of single steps), which costs three products for each one.
 // The plan depends on sizes, types and precision alone, not on the steps: so
 // does the workspace.  Measured: 8192 x 28672 58.0 against 77.3 ms, the seven
-// matrices of a TinyLlama layer 4.30 against 5.00 ms.
+// matrices of a TinyLlama layer 4.30 against 5.00 ms (both with tiles of 256).
 NsLayout layout_of(const lso_ns_params* p, bool all_bf16, const std::vector<Item>& items, NsCall& c)
 {
     const uint32_t precision = p ? p->precision : LSO_NS_AUTO;
@@ -323,8 +365,8 @@ NsLayout layout_of(const lso_ns_params* p, bool all_bf16, const std::vector<Item
         single += terms == 2 ? 3 * (6 * m * m * n + 2 * m * m * m) : 10 * m * m * n + 2 * m * m * m;
         pair += terms == 2 ? 3 * (3 * m * m * n + 5 * m * m * m) : 5 * m * m * n + 15 * m * m * m;
     }
-    // seven launches instead of six: small calls need a larger saving
-    c.pairs = pair * (tile_edge(items) == 64 ? 1.4 : 1.1) < single;
+    c.tile = tile_edge(items, single, pair);
+    c.pairs = pairs_pay(c.tile, single, pair);
     return c.pairs ? NsLayout{terms, 2, 4} : NsLayout{terms, terms, 2};
 }
 
@@ -349,7 +391,6 @@ uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<N
         for (const auto& o : order) sorted.push_back(items[o.second]);
         items.swap(sorted);
     }
-    c.tile = tile_edge(items);
     const uint64_t edge = c.tile;
     std::vector<Tiles> lists[4];
     uint64_t most_index = 0;
@@ -385,10 +426,10 @@ uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<N
                 // 32 where both operands have one term
                 const uint64_t gram = 16 * (3 - c.layout.x_terms) * ns_blocks(c.tile, true, c.layout.x_terms);
                 const uint64_t square = 16 * (3 - c.layout.square_terms) * ns_blocks(c.tile, true, c.layout.square_terms);
-                lists[0].push_back({tm * (tm + 1) / 2, np / gram});
-                lists[1].push_back({tm * (tm + 1) / 2, mp / square});
-                lists[2].push_back({tm * tn, mp / 16});
-                lists[3].push_back({tm * tn, mp / 32});
+                lists[0].push_back({tm * (tm + 1) / 2, np / gram, 1});
+                lists[1].push_back({tm * (tm + 1) / 2, mp / square, 1});
+                lists[2].push_back({tm * tn, mp / 16, 1});
+                lists[3].push_back({tm * tn, mp / 32, 1});
             }
             ++count;
             most_index = std::max({most_index, chunks, prep, uint64_t{count} * 2});

@@ -187,10 +187,12 @@ def ortho64_gpu(x, steps=5, coef=COEF):
 
 @pytest.mark.parametrize("shapes", [
     [(300, 9001), (70, 4000)],          # long: steps in pairs, tiles of 64
-    [(2050, 2311)],                     # nearly square: single steps, tiles of 128
-    [(777, 9000), (9001, 1030)],        # steps in pairs, tiles of 128
-    [(4099, 4501)],                     # tiles of 256, single steps
-    [(12001, 3001)],                    # tiles of 256, steps in pairs
+    [(2050, 2311)],                     # nearly square: single steps, tiles of 64
+    [(777, 9000), (9001, 1030)],        # steps in pairs, tiles of 64
+    [(4099, 4501)],                     # tiles of 128, single steps
+    [(12001, 3001)],                    # tiles of 128, steps in pairs
+    [(5050, 5070)],                     # tiles of 256, single steps
+    [(16001, 4090), (257, 300)],        # tiles of 256, steps in pairs
 ])
 @pytest.mark.parametrize("precision", [lso.LSO_NS_FULL, lso.LSO_NS_HALF])
 def test_orthogonalize_large(shapes, precision):
