@@ -48,13 +48,14 @@ extern "C" {
  * (S of the next step follows from the polynomial and S).
  * Matrices whose smaller side is at most LSO_NS_SMALL_SIDE take another way
  * whatever the precision: S is iterated on in FP64 and x multiplied once.
+ * (Those above 32 do not where a few of them come with larger matrices.)
  * A matrix with a NaN or an infinity gives NaNs (in that matrix only); a
  * zero matrix gives zeros.
  * ------------------------------------------------------------------- */
 #define LSO_NS_AUTO 0u
 #define LSO_NS_FULL 1u
 #define LSO_NS_HALF 2u
-#define LSO_NS_SMALL_SIDE 32u
+#define LSO_NS_SMALL_SIDE 64u
 #define LSO_NS_MAX_STEPS 16u
 
 /* The iteration.  NULL in a call means the defaults.  steps: 1 to

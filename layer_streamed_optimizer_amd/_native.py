@@ -99,7 +99,7 @@ class LsoFileLayer(ctypes.Structure):
 
 LSO_DT_I32, LSO_DT_I64 = 3, 4
 LSO_NS_AUTO, LSO_NS_FULL, LSO_NS_HALF = 0, 1, 2
-LSO_NS_SMALL_SIDE, LSO_NS_MAX_STEPS = 32, 16
+LSO_NS_SMALL_SIDE, LSO_NS_MAX_STEPS = 64, 16
 LSO_MUON_NESTEROV = 1
 LSO_EMBED_ADD = 1
 

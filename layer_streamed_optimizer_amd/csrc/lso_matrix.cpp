@@ -25,7 +25,28 @@ struct Item {
 
 uint64_t padded(uint64_t n, uint64_t tile) { return (n + tile - 1) / tile * tile; }
 
-int small_class(uint64_t k) { return k <= 8 ? 0 : k <= 16 ? 1 : k <= LSO_NS_SMALL_SIDE ? 2 : -1; }
+// The largest smaller side that takes the small path: 64, but 32 where the
+// launches of the general path are made anyway, for larger matrices, and
+// those of 33 to 64 have less than kApart elements along their long sides.
+// Measured (us, with the general path for those / apart from it): 6 of
+// 1024 x 1024 with 4, 16, 32 and 64 of 64 x 2048 672 / 746, 719 / 748, 784 / 756, 918 / 791;
+// one of 100 x 100 with 16, 32 and 64 of them 138 / 161, 162 / 168, 240 / 200.
+constexpr uint64_t kApart = 65536;
+
+uint64_t small_side(const std::vector<Item>& items)
+{
+    bool larger = false;
+    uint64_t length = 0;
+    for (const Item& it : items) {
+        const uint64_t k = std::min(it.rows, it.cols);
+        if (k > LSO_NS_SMALL_SIDE) larger = true;
+        else if (k > 32) length += std::max(it.rows, it.cols);
+    }
+    return larger && length < kApart ? 32 : LSO_NS_SMALL_SIDE;
+}
+
+// Which of the small path's kernels, -1 for none.
+int small_class(uint64_t k, uint64_t side) { return k > side ? -1 : k <= 8 ? 0 : k <= 16 ? 1 : k <= 32 ? 2 : 3; }
 
 // The largest values that a run from s <= 1 can meet: of the iterates'
 // singular values s, of s^2 and of the polynomial a + b s^2 + c s^4; and for
@@ -309,14 +330,14 @@ bool pairs_pay(uint32_t edge, double single, double pair) { return pair * (edge 
 // half of diagonal tiles, and fill and drain their pipeline sooner.  The edge
 // is the one whose launches of five steps cost least: a tile costs its stages
 // and `tile` more, a launch `launch` stages of latency, and `slots` workgroups
-// take `us` for a stage.  The numbers are fitted to 112 measured calls, one
-// to 1120 matrices of 33 x 4096 to 8192 x 8192 in both precisions, whose time is
-// 1.1% over the best edge's in the mean and 11% at most (a rule by the operations
-// of a step alone was 4.3% over and up to twice).  Measured (us, edges 64 / 128 /
-// 256): 22 of 256 x 2048 in half precision 301 / 383 / 600; in full precision
-// 1120 of 64 x 4096 6770 / 13778 / 43963, 2048 x 2048 850 / 777 / 1349, the seven of a
-// TinyLlama layer 5977 / 4003 / 4220, three of 4096 x 4096 15106 / 11164 / 10441.
-uint32_t tile_edge(const std::vector<Item>& items, double single, double pair)
+// take `us` for a stage.  The numbers are fitted to 100 measured calls, one
+// to 200 matrices of 100 x 2000 to 8192 x 8192 in both precisions, whose time is
+// 1.2% over the best edge's in the mean and 11% at most (a rule by the operations
+// of a step alone: 2.3% and 29%).  Measured (us, edges 64 / 128 / 256): 22 of
+// 256 x 2048 in half precision 301 / 383 / 600; in full precision 200 of 300 x 900 2264 /
+// 2910 / 6726, 2048 x 2048 850 / 777 / 1349, the seven of a TinyLlama layer 5977 / 4003 /
+// 4220, three of 4096 x 4096 15106 / 11164 / 10441.
+uint32_t tile_edge(const std::vector<Item>& items, uint64_t side, double single, double pair)
 {
     constexpr struct { uint32_t edge; double slots, tile, launch, us; } edges[3] = {
         {64, 1024, 32, 24, 0.29}, {128, 512, 80, 80, 0.286}, {256, 256, 128, 160, 0.4}};
@@ -329,7 +350,7 @@ uint32_t tile_edge(const std::vector<Item>& items, double single, double pair)
         double stages = 0.0;
         for (const Item& it : items) {
             const uint64_t k = std::min(it.rows, it.cols), l = std::max(it.rows, it.cols);
-            if (small_class(k) >= 0) continue;
+            if (k <= side) continue;
             const double tm = static_cast<double>((k + x.edge - 1) / x.edge), tn = static_cast<double>((l + x.edge - 1) / x.edge);
             const double half = tm * (tm + 1) / 2, m = tm * x.edge / 16 + x.tile, n = tn * x.edge / 16 + x.tile;
             stages += grams * half * n + squares * half * m + applies * tm * tn * m;
@@ -358,14 +379,15 @@ NsLayout layout_of(const lso_ns_params* p, bool all_bf16, const std::vector<Item
 {
     const uint32_t precision = p ? p->precision : LSO_NS_AUTO;
     const uint32_t terms = precision == LSO_NS_FULL || (precision == LSO_NS_AUTO && !all_bf16) ? 2 : 1;
+    const uint64_t side = small_side(items);
     double single = 0.0, pair = 0.0;   // matrix-core products of two steps
     for (const Item& it : items) {
         const double m = static_cast<double>(std::min(it.rows, it.cols)), n = static_cast<double>(std::max(it.rows, it.cols));
-        if (small_class(std::min(it.rows, it.cols)) >= 0) continue;
+        if (std::min(it.rows, it.cols) <= side) continue;
         single += terms == 2 ? 3 * (6 * m * m * n + 2 * m * m * m) : 10 * m * m * n + 2 * m * m * m;
         pair += terms == 2 ? 3 * (3 * m * m * n + 5 * m * m * m) : 5 * m * m * n + 15 * m * m * m;
     }
-    c.tile = tile_edge(items, single, pair);
+    c.tile = tile_edge(items, side, single, pair);
     c.pairs = pairs_pay(c.tile, single, pair);
     return c.pairs ? NsLayout{terms, 2, 4} : NsLayout{terms, terms, 2};
 }
@@ -391,7 +413,7 @@ uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<N
         for (const auto& o : order) sorted.push_back(items[o.second]);
         items.swap(sorted);
     }
-    const uint64_t edge = c.tile;
+    const uint64_t edge = c.tile, side = small_side(items);
     std::vector<Tiles> lists[4];
     uint64_t most_index = 0;
     for (int cls = 0; cls <= kNsClasses; ++cls) {
@@ -399,7 +421,7 @@ uint64_t plan(std::vector<Item>& items, NsCall& c, uintptr_t work, std::vector<N
         uint32_t count = 0;
         for (const Item& it : items) {
             const uint64_t k = std::min(it.rows, it.cols), l = std::max(it.rows, it.cols);
-            const int own = small_class(k);
+            const int own = small_class(k, side);
             if ((own < 0 ? kNsClasses : own) != cls) continue;
             NsMat m = it.mat;
             m.rows = static_cast<uint32_t>(it.rows);

@@ -18,8 +18,8 @@ constexpr double kNsMostValue = 15.9;
 constexpr uint32_t kNsPrep = 64;
 // Elements along the long side per workgroup of the small path.
 constexpr uint32_t kNsSmallChunk = 256;
-// The small path's kernels are built for smaller sides up to 8, 16 and 32.
-constexpr int kNsClasses = 3;
+// The small path's kernels are built for smaller sides up to 8, 16, 32 and 64.
+constexpr int kNsClasses = 4;
 constexpr uint32_t kNsMaxSteps = 16;
 
 enum : uint32_t {
@@ -87,7 +87,7 @@ inline NsWork ns_work(uint64_t mp, uint64_t np, const NsLayout& l)
 // k x k matrix that x is multiplied by, in rows of its class's size.
 inline uint64_t ns_small_bytes(uint64_t k, uint64_t l)
 {
-    const uint64_t chunks = (l + kNsSmallChunk - 1) / kNsSmallChunk, side = k <= 8 ? 8 : k <= 16 ? 16 : 32;
+    const uint64_t chunks = (l + kNsSmallChunk - 1) / kNsSmallChunk, side = k <= 8 ? 8 : k <= 16 ? 16 : k <= 32 ? 32 : 64;
     return (chunks * k * k * 8 + side * side * 8 + 255) / 256 * 256;
 }
 

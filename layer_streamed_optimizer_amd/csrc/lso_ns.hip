@@ -1,7 +1,7 @@
 // Newton-Schulz orthogonalisation and the orthogonalised-momentum update for
 // gfx950.  Formulas and precisions: lso_ops.h.
 //
-// General path (smaller side above 32), all matrices of a call together, one
+// General path (smaller side above 64), all matrices of a call together, one
 // launch per step below:
 //   norm     u (for the update: m' and u), its sum of squares per tile
 //   scale    1 / (|u|_F + eps) per matrix
@@ -889,7 +889,10 @@ __global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(co
 // S_0 squares the singular values' spread and each step multiplies the
 // error of the small ones by a^2 (about 12), which FP32 would not survive
 // over five steps; in FP64 it ends near 1e-11.  |u|_F^2 is the trace of the
-// unscaled S.  Bound: two reads of u and launch latency.
+// unscaled S.  Bound: two reads of u and launch latency; for sides of 33 to
+// 64 the FP64 matrix instructions.  Measured (us) for those, here and in the
+// general path in full precision: 308 of 64 x 2048 411 / 915, 2000 of 64 x 512 862 /
+// 3045, one of 64 x 4096 75 / 106, of 64 x 262144 447 / 827, two of 64 x 64 68 / 68.
 
 constexpr uint32_t kSmallPitch = kNsSmallChunk + 1;
 
@@ -934,18 +937,40 @@ __global__ void __launch_bounds__(256) ns_small_gram_kernel(const NsMat* tab, ui
     // FP64 matrix instructions: 16 x 16 products of 16 rows by 4 values, the
     // same register for both operands.  With kK = 8 rows 8 to 15 are the
     // first eight again at the other half of the chunk; with 32 the tiles
-    // are (0, 0), (0, 1) and (1, 1).  (A thread per product, with FP64 vector
+    // are (0, 0), (0, 1) and (1, 1); with 64 a wave makes a row of four tiles
+    // from the whole chunk.  (A thread per product, with FP64 vector
     // instructions, took 14.4 against 13.2 us for 308 adapters: two loads
     // and two conversions for each.)
     constexpr int kTiles = kK == 32 ? 3 : 1, kRows = kK == 32 ? 2 : 1;
     constexpr uint32_t kSpan = kK == 8 ? kNsSmallChunk / 2 : kNsSmallChunk;   // values per row
     __shared__ float u[kK * kSmallPitch];
-    __shared__ double part[kTiles * 4 * 256];   // [tile][wave][row][column]
+    __shared__ double part[kK == 64 ? 1 : kTiles * 4 * 256];   // [tile][wave][row][column]
     const NsMat m = load_mat(tab, find_mat<&NsMat::prep0>(tab, n, index, blockIdx.x));
     const uint32_t chunk = blockIdx.x - m.prep0, k = m.rows < m.cols ? m.rows : m.cols;
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     stage_u<kK, true>(m, chunk * kNsSmallChunk, u);
     __syncthreads();
+    double* out = reinterpret_cast<double*>(m.work) + static_cast<uint64_t>(chunk) * k * k;
+    if constexpr (kK == 64) {
+        f64x4 sum[4] = {};
+        const float* from = u + (lane & 15u) * kSmallPitch + (lane >> 4);
+        const float* mine = from + wave * 16 * kSmallPitch;
+#pragma unroll 4
+        for (uint32_t x = 0; x < kNsSmallChunk; x += 4) {
+            const double row = mine[x];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                sum[y] = __builtin_amdgcn_mfma_f64_16x16x4f64(row, static_cast<double>(from[y * 16 * kSmallPitch + x]), sum[y], 0, 0, 0);
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t p = wave * 16 + 4 * e + (lane >> 4), q = y * 16 + (lane & 15u);
+                if (p < k && q < k) out[p * k + q] = sum[y][e];
+            }
+        return;
+    }
     f64x4 acc[kTiles] = {};
     const uint32_t row = lane & 15u, at = wave * (kSpan / 4) + (lane >> 4);
     const float* from = kK == 8 ? u + (row & 7u) * kSmallPitch + (row >> 3) * kSpan + at : u + row * kSmallPitch + at;
@@ -966,7 +991,6 @@ __global__ void __launch_bounds__(256) ns_small_gram_kernel(const NsMat* tab, ui
 #pragma unroll
         for (int e = 0; e < 4; ++e) part[((y * 4 + wave) * 16 + 4 * e + (lane >> 4)) * 16 + (lane & 15u)] = acc[y][e];
     __syncthreads();
-    double* out = reinterpret_cast<double*>(m.work) + static_cast<uint64_t>(chunk) * k * k;
     for (uint32_t v = threadIdx.x; v < kK * kK; v += 256) {
         uint32_t p = v / kK, q = v % kK;
         if (p >= k || q >= k) continue;
@@ -997,11 +1021,15 @@ struct SmallArgs {
     double coef[3 * kNsMaxSteps];
 };
 
-// One workgroup per matrix.  kK = 8: a thread per element.  kK = 16 and 32: a
-// wave per 16 x 16 tile, FP64 matrix instructions (32 x 32: 26 against 12 us
+// Threads of a workgroup of it.
+constexpr int small_threads(int k) { return k == 64 ? 640 : k == 32 ? 256 : 64; }
+
+// One workgroup per matrix.  kK = 8: a thread per element.  kK = 16 to 64: a
+// wave per 16 x 16 tile (of 64 x 64 on and under the diagonal, as all of these
+// are polynomials in S), FP64 matrix instructions (32 x 32: 26 against 12 us
 // with two by two elements per thread).
 template <int kK>
-__global__ void __launch_bounds__(kK == 32 ? 256 : 64) ns_small_iterate_kernel(const SmallArgs args)
+__global__ void __launch_bounds__(small_threads(kK)) ns_small_iterate_kernel(const SmallArgs args)
 {
     constexpr int kE = kK == 8 ? 1 : 4;   // elements per thread
     __shared__ double s[kK][kK + 1], t[kK][kK + 1], p[kK][kK + 1], q[kK][kK + 1];
@@ -1009,9 +1037,23 @@ __global__ void __launch_bounds__(kK == 32 ? 256 : 64) ns_small_iterate_kernel(c
     const uint32_t k = m.rows < m.cols ? m.rows : m.cols, l = m.rows < m.cols ? m.cols : m.rows;
     const uint32_t chunks = (l + kNsSmallChunk - 1) / kNsSmallChunk;
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+    // the wave's tile
+    uint32_t ti = kK == 32 ? wave >> 1 : 0, tj = kK == 32 ? wave & 1u : wave;
+    if (kK == 64) {
+        for (; tj > ti; ++ti) tj -= ti + 1;
+    }
+    ti *= 16;
+    tj *= 16;
     // element e of a thread: row i + e * 4, column j
-    const uint32_t i = kK == 8 ? lane >> 3 : (wave >> 1) * 16 + (lane >> 4), j = kK == 8 ? lane & 7u : (wave & 1u) * 16 + (lane & 15u);
+    const uint32_t i = kK == 8 ? lane >> 3 : ti + (lane >> 4), j = kK == 8 ? lane & 7u : tj + (lane & 15u);
     const double* part = reinterpret_cast<const double*>(m.work);
+    auto put = [&](double (&to)[kK][kK + 1], const double (&from)[kE]) {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+            to[i + e * 4][j] = from[e];
+            if (kK == 64 && ti != tj) to[j][i + e * 4] = from[e];
+        }
+    };
     double v[kE];
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
@@ -1023,18 +1065,14 @@ __global__ void __launch_bounds__(kK == 32 ? 256 : 64) ns_small_iterate_kernel(c
             for (uint32_t c = 0; c < chunks; ++c) sum += from[static_cast<uint64_t>(c) * k * k];
         }
         v[e] = sum;
-        s[ii][j] = sum;
     }
+    put(s, v);
     __syncthreads();
     double trace = 0.0;
 #pragma unroll
     for (int x = 0; x < kK; ++x) trace += s[x][x];   // zeros from k on
     const double inv = 1.0 / (sqrt(trace) + args.eps);
     __syncthreads();
-    auto put = [&](double (&to)[kK][kK + 1], const double (&from)[kE]) {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) to[i + e * 4][j] = from[e];
-    };
     auto product = [&](const double (&a)[kK][kK + 1], const double (&b)[kK][kK + 1], double (&out)[kE]) {
         if constexpr (kK == 8) {
             double sum = 0.0;
@@ -1045,7 +1083,7 @@ __global__ void __launch_bounds__(kK == 32 ? 256 : 64) ns_small_iterate_kernel(c
             f64x4 sum = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
             for (uint32_t e = 0; e < kK; e += 4)
-                sum = __builtin_amdgcn_mfma_f64_16x16x4f64(a[(wave >> 1) * 16 + (lane & 15u)][e + (lane >> 4)],
+                sum = __builtin_amdgcn_mfma_f64_16x16x4f64(a[ti + (lane & 15u)][e + (lane >> 4)],
                                                            b[e + (lane >> 4)][j], sum, 0, 0, 0);
 #pragma unroll
             for (int e = 0; e < kE; ++e) out[e] = sum[e];
@@ -1067,18 +1105,22 @@ __global__ void __launch_bounds__(kK == 32 ? 256 : 64) ns_small_iterate_kernel(c
         for (int e = 0; e < kE; ++e) w[e] = (i + e * 4 == j ? a : 0.0) + b * s[i + e * 4][j] + c * w[e];
         put(p, w);
         __syncthreads();
-        product(p, s, w);
-        put(t, w);
+        const bool more = n + 1 < args.steps;
+        if (more) {
+            product(p, s, w);
+            put(t, w);
+        }
         product(p, q, w);
         __syncthreads();
         put(q, w);
-        product(t, p, w);
-        put(s, w);
+        if (more) {
+            product(t, p, w);
+            put(s, w);
+        }
         __syncthreads();
     }
     double* out = reinterpret_cast<double*>(m.work) + static_cast<uint64_t>(chunks) * k * k;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) out[(i + e * 4) * kK + j] = q[i + e * 4][j];   // zeros from k on
+    for (uint32_t x = threadIdx.x; x < kK * kK; x += small_threads(kK)) out[x] = q[x / kK][x % kK];   // zeros from k on
 }
 
 template <int kK>
@@ -1090,9 +1132,10 @@ __global__ void __launch_bounds__(256) ns_small_apply_kernel(const NsMat* tab, u
     const uint32_t k = m.rows < m.cols ? m.rows : m.cols, l = m.rows < m.cols ? m.cols : m.rows;
     const uint32_t chunks = (l + kNsSmallChunk - 1) / kNsSmallChunk;
     const bool tall = (m.flags & kNsTall) != 0;
-    __shared__ double q[kK * kK];
+    constexpr uint32_t kPitch = kK == 64 ? kK + 1 : kK;
+    __shared__ double q[kK * kPitch];
     const double* src = reinterpret_cast<const double*>(m.work) + static_cast<uint64_t>(chunks) * k * k;
-    for (uint32_t v = threadIdx.x; v < kK * kK; v += 256) q[v] = src[v];
+    for (uint32_t v = threadIdx.x; v < kK * kK; v += 256) q[v / kK * kPitch + v % kK] = src[v];
     constexpr int kQuads = kK / 4;
     f32x4 old[kQuads];
 #pragma unroll
@@ -1103,20 +1146,46 @@ __global__ void __launch_bounds__(256) ns_small_apply_kernel(const NsMat* tab, u
     }
     stage_u<kK, false>(m, l0, u);
     __syncthreads();
-    // one column of u per thread, four rows of the result at a time
-    float col[kK];
+    if constexpr (kK == 64) {
+        // a wave's 64 columns of u, which no other wave touches: a tile of
+        // four by four matrix instructions' results (a thread per column
+        // would wait for LDS, two reads of q for each four products)
+        const uint32_t lane = threadIdx.x & 63u, c0 = (threadIdx.x & ~63u) + (lane & 15u), e0 = lane >> 4;
+        f64x4 sum[4][4] = {};
+        for (uint32_t e = 0; e < kK; e += 4) {
+            double a[4], b[4];
 #pragma unroll
-    for (int e = 0; e < kK; ++e) col[e] = u[e * kSmallPitch + threadIdx.x];
-    for (uint32_t p = 0; p < k; p += 4) {
-        double v[4] = {0.0, 0.0, 0.0, 0.0};
+            for (int y = 0; y < 4; ++y) {
+                a[y] = q[(y * 16 + (lane & 15u)) * kPitch + e + e0];
+                b[y] = u[(e + e0) * kSmallPitch + c0 + y * 16];
+            }
 #pragma unroll
-        for (int e = 0; e < kK; ++e) {
-            const double x = col[e];
+            for (int y = 0; y < 4; ++y)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) v[y] = fma(q[(p + y) * kK + e], x, v[y]);
+                for (int x = 0; x < 4; ++x) sum[y][x] = __builtin_amdgcn_mfma_f64_16x16x4f64(a[y], b[x], sum[y][x], 0, 0, 0);
         }
 #pragma unroll
-        for (int y = 0; y < 4; ++y) u[(p + y) * kSmallPitch + threadIdx.x] = static_cast<float>(v[y]);
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[(y * 16 + 4 * e + e0) * kSmallPitch + c0 + x * 16] = static_cast<float>(sum[y][x][e]);
+    } else {
+        // one column of u per thread, four rows of the result at a time
+        float col[kK];
+#pragma unroll
+        for (int e = 0; e < kK; ++e) col[e] = u[e * kSmallPitch + threadIdx.x];
+        for (uint32_t p = 0; p < k; p += 4) {
+            double v[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+            for (int e = 0; e < kK; ++e) {
+                const double x = col[e];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) v[y] = fma(q[(p + y) * kPitch + e], x, v[y]);
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) u[(p + y) * kSmallPitch + threadIdx.x] = static_cast<float>(v[y]);
+        }
     }
     __syncthreads();
 #pragma unroll
@@ -1139,7 +1208,7 @@ hipError_t launch_small(const NsCall& c, const NsMat* tab, uint32_t n, uint32_t 
     args.eps = c.eps;
     for (uint32_t k = 0; k < 3 * c.steps; ++k) args.coef[k] = c.coef[k];
     hipLaunchKernelGGL(ns_small_gram_kernel<kK>, dim3(chunks), dim3(256), 0, s, tab, n, index);
-    hipLaunchKernelGGL(ns_small_iterate_kernel<kK>, dim3(n), dim3(kK == 32 ? 256 : 64), 0, s, args);
+    hipLaunchKernelGGL(ns_small_iterate_kernel<kK>, dim3(n), dim3(small_threads(kK)), 0, s, args);
     hipLaunchKernelGGL(ns_small_apply_kernel<kK>, dim3(chunks), dim3(256), 0, s, tab, n, index);
     return hipGetLastError();
 }
@@ -1283,7 +1352,8 @@ int ns_launch(const NsCall& c, NsMat* device_table, void* stream)
         if (c.nsmall[k] == 0) continue;
         err = k == 0 ? launch_small<8>(c, tab, c.nsmall[k], c.small_chunks[k], c.small_index[k], s)
             : k == 1 ? launch_small<16>(c, tab, c.nsmall[k], c.small_chunks[k], c.small_index[k], s)
-                     : launch_small<32>(c, tab, c.nsmall[k], c.small_chunks[k], c.small_index[k], s);
+            : k == 2 ? launch_small<32>(c, tab, c.nsmall[k], c.small_chunks[k], c.small_index[k], s)
+                     : launch_small<64>(c, tab, c.nsmall[k], c.small_chunks[k], c.small_index[k], s);
         tab += c.nsmall[k];
     }
     if (err == hipSuccess && c.nbig > 0) {

@@ -14,7 +14,7 @@ of |y|_F.
         directions: eta = 2^-22 + 2^-24 sqrt(3 K / 16);
   half  S and the polynomial are rounded to 11 bits: at most 2^-12 each,
         2^-12 / sqrt(3) in the root mean square: eta = 2^-12 / sqrt(3).
-Smaller side up to 32: FP64 to the end, whose errors (2^-53, growing with the
+Smaller side up to 64: FP64 to the end, whose errors (2^-53, growing with the
 square of the amplification, at most 3.45^10 = 2.4e5) stay below 1e-9.
 Storing y rounds once, by half a step at most: FP32 has 24 significant bits,
 so neighbours in [1, 2) are 2^-23 apart and the rounding is at most 2^-24 of
@@ -148,6 +148,24 @@ def test_orthogonalize_shapes_in_one_call(precision, x_dtype, y_dtype):
     m = Mats(SHAPES, x_dtype, y_dtype, pad_x=5, pad_y=3)
     for (r, c), src, got in zip(SHAPES, m.src, run_ortho(m, precision=precision)):
         check(got, ortho64(src), r, c, precision == lso.LSO_NS_FULL, y_dtype == "bf16", f"{r}x{c}")
+
+
+@pytest.mark.parametrize("precision", [lso.LSO_NS_FULL, lso.LSO_NS_HALF])
+@pytest.mark.parametrize("kind", ["noise", "spiked"])
+def test_orthogonalize_sides_of_33_to_64_in_fp64(precision, kind):
+    """Smaller sides of 33 to 64 go the way of 32 and less, FP64 to the end
+    whatever the precision, alone and where they are long enough next to
+    larger matrices; a few of them go with the larger ones."""
+    few = [(33, 33), (33, 257), (64, 64), (64, 2048), (1000, 64), (63, 513), (48, 16384), (2049, 40), (40, 16385), (5, 9)]
+    for shapes, fp64 in ((few, True), (few + [(65, 100)], False), (few + [(30000, 40), (65, 100)], True)):
+        m = Mats(shapes, kind=kind, seed=17, pad_x=3, pad_y=1)
+        log(f"orthogonalize sides of 33 to 64, precision {precision}, {kind}, {len(shapes)} matrices")
+        for (r, c), src, got in zip(shapes, m.src, run_ortho(m, precision=precision)):
+            want = ortho64(src)
+            err = np.linalg.norm(got - want) / np.linalg.norm(want)
+            # twice the side of 32: twice the terms of a sum, under 4e-9 by the same count
+            allow = 4e-9 + 2.0**-24 if fp64 and min(r, c) <= 64 else tolerance(r, c, precision == lso.LSO_NS_FULL, False)
+            assert err <= allow, (r, c, err, allow)
 
 
 @pytest.mark.parametrize("rows,cols", [(8, 2048), (5632, 8), (40, 4099), (700, 300), (384, 1024)])
