@@ -111,11 +111,9 @@ def _gradient(gen, count, rows, cols):
 
 def _tokens(gen, n, vocab, dtype):
     """Token ids by a Zipf-like law over shuffled ids; about one in 64 positions is padding (-1)."""
-    # the distribution function is summed on the host: a device sum's order may vary, and with it the tokens of a seed
-    law = torch.cumsum(1.0 / (torch.arange(vocab, dtype=torch.float64) + 2.7), 0).cuda()
+    p = 1.0 / (torch.arange(vocab, device="cuda", dtype=torch.float32) + 2.7)
     ids = torch.randperm(vocab, generator=gen, device="cuda")
-    at = torch.searchsorted(law, torch.rand(n, generator=gen, device="cuda", dtype=torch.float64) * law[-1])
-    t = ids[at.clamp_(max=vocab - 1)]
+    t = ids[torch.multinomial(p, n, replacement=True, generator=gen)]
     t[torch.rand(n, generator=gen, device="cuda") < 1 / 64] = -1
     return t.to(dtype)
 
