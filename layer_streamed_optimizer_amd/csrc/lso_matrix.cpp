@@ -152,10 +152,9 @@ struct Arrays {
 };
 
 // The checks of lso_orthogonalize; with arrays, of its addresses too.
-lso_status collect(const lso_matrix* mats, size_t n, std::vector<Item>& items, Arrays* arrays, bool& all_bf16)
+lso_status collect(const lso_matrix* mats, size_t n, std::vector<Item>& items, Arrays* arrays)
 {
     if (n > 0 && !mats) return fail(LSO_E_INVALID, "mats is NULL");
-    all_bf16 = true;
     for (size_t i = 0; i < n; ++i) {
         const lso_matrix& a = mats[i];
         for (const uint32_t d : {a.x_dtype, a.y_dtype})
@@ -166,7 +165,6 @@ lso_status collect(const lso_matrix* mats, size_t n, std::vector<Item>& items, A
         if (a.rows == 0 || a.cols == 0) continue;
         if (a.ld_x < a.cols || a.ld_y < a.cols || a.ld_x > kMaxSide || a.ld_y > kMaxSide)
             return fail(LSO_E_INVALID, "matrix %zu: a row stride is smaller than cols, or too large", i);
-        if (a.y_dtype != LSO_DT_BF16) all_bf16 = false;
         const uint64_t ex = a.x_dtype == LSO_DT_F32 ? 4 : 2, ey = a.y_dtype == LSO_DT_F32 ? 4 : 2;
         if (arrays) {
             const bool same = a.x == a.y && a.x_dtype == a.y_dtype && a.ld_x == a.ld_y;
@@ -191,10 +189,9 @@ lso_status collect(const lso_matrix* mats, size_t n, std::vector<Item>& items, A
     return LSO_OK;
 }
 
-lso_status collect(const lso_muon_block* blocks, size_t n, std::vector<Item>& items, Arrays* arrays, bool& all_bf16)
+lso_status collect(const lso_muon_block* blocks, size_t n, std::vector<Item>& items, Arrays* arrays)
 {
     if (n > 0 && !blocks) return fail(LSO_E_INVALID, "blocks is NULL");
-    all_bf16 = false;   // the result is the FP32 master
     for (size_t i = 0; i < n; ++i) {
         const lso_muon_block& b = blocks[i];
         if (b.grad_dtype != LSO_DT_BF16 && b.grad_dtype != LSO_DT_F32)
@@ -372,13 +369,12 @@ uint32_t tile_edge(const std::vector<Item>& items, uint64_t side, double single,
 // the next X with itself as rounding makes that one.  In half precision the
 // squares keep two terms then (with one the error grows, with two it falls
 // below that of single steps), which costs three products for each one.
-// The plan depends on sizes, types and precision alone, not on the steps: so
-// does the workspace.  Measured: 8192 x 28672 58.0 against 77.3 ms, the seven
+// The plan depends on sizes and precision alone, not on the steps: so does the
+// workspace.  Measured: 8192 x 28672 58.0 against 77.3 ms, the seven
 // matrices of a TinyLlama layer 4.30 against 5.00 ms (both with tiles of 256).
-NsLayout layout_of(const lso_ns_params* p, bool all_bf16, const std::vector<Item>& items, NsCall& c)
+NsLayout layout_of(const lso_ns_params* p, const std::vector<Item>& items, NsCall& c)
 {
-    const uint32_t precision = p ? p->precision : LSO_NS_AUTO;
-    const uint32_t terms = precision == LSO_NS_FULL || (precision == LSO_NS_AUTO && !all_bf16) ? 2 : 1;
+    const uint32_t terms = p && p->precision == LSO_NS_HALF ? 1 : 2;
     const uint64_t side = small_side(items);
     double single = 0.0, pair = 0.0;   // matrix-core products of two steps
     for (const Item& it : items) {
@@ -516,9 +512,8 @@ uint64_t workspace_bytes(const T* list, size_t n, const lso_ns_params* params)
     NsCall c{};
     std::vector<Item> items;
     std::vector<NsMat> table;
-    bool all_bf16;
-    if (check_params(params, c) != LSO_OK || collect(list, n, items, nullptr, all_bf16) != LSO_OK) return 0;
-    c.layout = layout_of(params, all_bf16, items, c);
+    if (check_params(params, c) != LSO_OK || collect(list, n, items, nullptr) != LSO_OK) return 0;
+    c.layout = layout_of(params, items, c);
     return plan(items, c, 0, table);
 }
 
@@ -530,13 +525,12 @@ lso_status run(const T* list, size_t n, const lso_ns_params* params, void* works
     std::vector<Item> items;
     std::vector<NsMat> table;
     Arrays arrays;
-    bool all_bf16;
     items.reserve(n < 65536 ? n : 65536);
     lso_status s = check_params(params, c);
-    if (s == LSO_OK) s = collect(list, n, items, &arrays, all_bf16);
+    if (s == LSO_OK) s = collect(list, n, items, &arrays);
     if (s != LSO_OK) return s;
     if (items.empty()) return LSO_OK;
-    c.layout = layout_of(params, all_bf16, items, c);
+    c.layout = layout_of(params, items, c);
     if (!workspace) return fail(LSO_E_INVALID, "workspace is NULL");
     if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return fail(LSO_E_ALIGN, "workspace must be 16-byte aligned");
     const uint64_t need = plan(items, c, reinterpret_cast<uintptr_t>(workspace), table);

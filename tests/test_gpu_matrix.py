@@ -571,3 +571,22 @@ def test_errors_leave_the_thread_usable():
     run_muon(b)
     b.check()
     assert lib.lso_muon_step(ctypes.c_void_p(b.table.ptr), 1, None, None, 0, None) == 1
+
+
+def test_auto_precision_is_full_for_bf16_results():
+    """A BF16 matrix orthogonalised without naming a precision: the bits of
+    full precision, and next to nothing but the result's own rounding off the
+    definition.  A value within the error e of full precision (its norm-wise
+    bound, three times over for a single element) of a midpoint of two BF16
+    numbers may round to the other one, a step of 2^-7 of the value at most."""
+    shapes = [(256, 500), (900, 200)]
+    auto, full = Mats(shapes, "bf16", "bf16", seed=21), Mats(shapes, "bf16", "bf16", seed=21)
+    log("orthogonalize BF16 with AUTO and FULL")
+    a, f = run_ortho(auto), run_ortho(full, precision=lso.LSO_NS_FULL)
+    for (r, c), src, x, y in zip(shapes, auto.src, a, f):
+        assert np.array_equal(x, y)
+        want = ortho64(src)
+        rounded = (bf16(want.astype(np.float32)).astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+        share = 3 * tolerance(r, c, True, False) * np.linalg.norm(want) / math.sqrt(want.size)
+        off = np.abs(x - rounded)
+        assert np.all(off <= 2.0**-7 * np.abs(want) + share)

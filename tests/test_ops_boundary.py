@@ -253,3 +253,11 @@ def test_table_rows():
     assert np.all(tab.arr["lr"] == 0.5)
     one = lso.MatrixTable.from_rows([mat(), mat(1, ld_x=300)])
     assert one.arr["ld_x"].tolist() == [200, 300] and one.arr["ld_y"].tolist() == [200, 200]
+
+
+def test_half_precision_is_the_callers_choice():
+    """AUTO plans as FULL does, BF16 results or not."""
+    for y_dtype in (lso.LSO_DT_F32, lso.LSO_DT_BF16):
+        tab = lso.MatrixTable.from_rows([mat(x_dtype=lso.LSO_DT_BF16, y_dtype=y_dtype), mat(1, x_dtype=lso.LSO_DT_BF16, y_dtype=y_dtype)])
+        full, half = (lso.orthogonalize_workspace_bytes(tab, p) for p in (lso.LSO_NS_FULL, lso.LSO_NS_HALF))
+        assert lso.orthogonalize_workspace_bytes(tab) == full > half
