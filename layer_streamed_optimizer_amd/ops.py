@@ -38,21 +38,93 @@ def dtype_of(tensor) -> int:
     return code
 
 
+def _array(x, name: str, code: int | None, default: int, rows: int, cols: int, ld: int | None = None) -> tuple:
+    """(address, LSO_DT_* code, row stride) of a matrix's array.  An address
+    has the type and stride that are given, or `default` and cols.  A torch
+    tensor of shape [rows, cols] brings both; any contiguous one that holds
+    them may stand for the rows at stride ld, and one of integers of the same
+    size for their bits.  What contradicts the tensor is refused."""
+    if x is None or isinstance(x, int):
+        return x or 0, default if code is None else code, cols if ld is None else ld
+    addr, dtype = x.data_ptr(), x.dtype
+    if code is None or dtype.is_floating_point:
+        own = dtype_of(x)
+        if own != LSO_DT_F32 and own != LSO_DT_BF16 or code is not None and code != own:
+            raise TypeError(f"{name}: a tensor of {dtype}" + ("" if code is None else f" given as type code {code}"))
+    else:
+        own = code
+        if x.element_size() != (4 if code == LSO_DT_F32 else 2):
+            raise TypeError(f"{name}: a tensor of {x.dtype} cannot hold the bits of type code {code}")
+    if rows == 0 or cols == 0:
+        return addr, own, cols if ld is None else ld
+    if x.shape == (rows, cols):
+        in_rows, in_cols = x.stride()
+        if cols > 1 and in_cols != 1:
+            raise ValueError(f"{name}: the elements of a row must be contiguous (strides {in_rows}, {in_cols})")
+        if rows > 1:
+            if ld is not None and ld != in_rows:
+                raise ValueError(f"{name}: row stride {ld} given for a tensor of row stride {in_rows}")
+            ld = in_rows
+    elif not x.is_contiguous() or x.numel() < (rows - 1) * (cols if ld is None else ld) + cols:
+        raise ValueError(f"{name}: a tensor of shape {tuple(x.shape)} and strides {x.stride()} does not hold {rows} x {cols}")
+    return addr, own, cols if ld is None else ld
+
+
+def _gpu(x, name: str) -> int | None:
+    """The GPU of a torch tensor; None for an address."""
+    if x is None or isinstance(x, int):
+        return None
+    if not x.is_cuda:
+        raise ValueError(f"{name} is on {x.device}, not on a GPU")
+    return x.get_device()
+
+
+def _check_device(device: int | None) -> None:
+    """device: of a call's tensors, or None."""
+    if device is None:
+        return
+    global _current_device
+    if _current_device is None:
+        import torch
+        _current_device = torch.cuda.current_device
+    if device != _current_device():
+        raise ValueError(f"the tensors are on GPU {device}, which is not the current device")
+
+
+_current_device = None
+
+
 class _Table:
+    """Rows hold addresses: the tensors that they were made from must live as
+    long as the table is used."""
+
     DTYPE: np.dtype
 
     def __init__(self, n: int):
         self.arr = np.zeros(n, self.DTYPE)
+        self.device: int | None = None     # of the tensors that its rows were made from
 
     def __len__(self) -> int:
         return len(self.arr)
 
     @classmethod
     def from_rows(cls, rows: Iterable[dict]):
-        fields = [cls._fields(**r) for r in rows]
-        tab = cls(len(fields))
-        tab.arr[:] = fields
+        rows = list(rows)
+        tab = cls(len(rows))
+        tab.arr[:] = [tab._row(**r) for r in rows]
         return tab
+
+    def _row(self, **row) -> tuple:
+        fields, arrays = self._fields(**row)
+        for name, x in arrays:
+            device = _gpu(x, name)
+            if device is None:
+                continue
+            if self.device is None:
+                self.device = device
+            elif device != self.device:
+                raise ValueError(f"{name} is on GPU {device}, the table's other tensors on GPU {self.device}")
+        return fields
 
     @property
     def ptr(self) -> int:
@@ -65,14 +137,17 @@ class MatrixTable(_Table):
     DTYPE = MATRIX_DTYPE
 
     @staticmethod
-    def _fields(*, x, y, rows: int, cols: int, ld_x: int | None = None, ld_y: int | None = None, x_dtype: int = LSO_DT_F32,
-                y_dtype: int = LSO_DT_F32) -> tuple:
-        return (_addr(x), _addr(y), rows, cols, cols if ld_x is None else ld_x, cols if ld_y is None else ld_y, x_dtype, y_dtype)
+    def _fields(*, x, y, rows: int, cols: int, ld_x: int | None = None, ld_y: int | None = None, x_dtype: int | None = None,
+                y_dtype: int | None = None) -> tuple:
+        ax, tx, lx = _array(x, "x", x_dtype, LSO_DT_F32, rows, cols, ld_x)
+        ay, ty, ly = _array(y, "y", y_dtype, LSO_DT_F32, rows, cols, ld_y)
+        return (ax, ay, rows, cols, lx, ly, tx, ty), (("x", x), ("y", y))
 
     def set_row(self, i: int, **row) -> None:
-        """x, y (torch tensors, by their data_ptr, or device addresses), rows,
-        cols, ld_x, ld_y (default cols), x_dtype, y_dtype (default FP32)."""
-        self.arr[i] = self._fields(**row)
+        """x, y, rows, cols, ld_x, ld_y, x_dtype, y_dtype.  x and y are torch
+        tensors, which bring their type and row stride, or device addresses
+        (FP32 and cols unless given)."""
+        self.arr[i] = self._row(**row)
 
 
 class MuonTable(_Table):
@@ -82,17 +157,29 @@ class MuonTable(_Table):
     DTYPE = MUON_DTYPE
 
     @staticmethod
-    def _fields(*, rows: int, cols: int, master, m, grad, weight=None, base: int = 0, grad_dtype: int = LSO_DT_BF16,
+    def _fields(*, rows: int, cols: int, master, m, grad, weight=None, base: int = 0, grad_dtype: int | None = None,
                 nesterov: bool = True, lr: float = 1e-3, beta: float = 0.95, weight_decay: float = 0.0, scale: float = 1.0) -> tuple:
-        return (base, rows, cols, _addr(master), _addr(m), _addr(grad), _addr(weight), grad_dtype,
-                LSO_DT_BF16 if weight is not None else LSO_DT_NONE, LSO_MUON_NESTEROV if nesterov else 0, 0, lr, beta, weight_decay,
-                scale)
+        arrays = (("master", master), ("m", m), ("grad", grad), ("weight", weight))
+        addr = []
+        for (name, a), code, default in zip(arrays, (LSO_DT_F32, LSO_DT_F32, grad_dtype, LSO_DT_BF16),
+                                            (LSO_DT_F32, LSO_DT_F32, LSO_DT_BF16, LSO_DT_BF16)):
+            at, own, ld = _array(a, name, code, default, rows, cols)
+            if ld != cols and rows > 1:
+                raise ValueError(f"{name} must be contiguous (row stride {ld})")
+            if base != 0 and a is not None and not isinstance(a, int):
+                raise ValueError(f"{name}: with a base, arrays are offsets from it, not tensors")
+            addr.append(at)
+            if name == "grad":
+                grad_dtype = own
+        return (base, rows, cols, *addr, grad_dtype, LSO_DT_BF16 if weight is not None else LSO_DT_NONE,
+                LSO_MUON_NESTEROV if nesterov else 0, 0, lr, beta, weight_decay, scale), arrays
 
     def set_row(self, i: int, **row) -> None:
-        """rows, cols; master, m, grad and weight (or None): torch tensors or
-        device addresses (offsets from base if base != 0); grad_dtype,
-        nesterov, lr, beta, weight_decay, scale."""
-        self.arr[i] = self._fields(**row)
+        """rows, cols; master, m, grad and weight (or None): contiguous torch
+        tensors or device addresses (offsets from base if base != 0);
+        grad_dtype (the tensor's, or BF16 for an address), nesterov, lr, beta,
+        weight_decay, scale."""
+        self.arr[i] = self._row(**row)
 
     def set_lr(self, lr: float) -> None:
         self.arr["lr"] = lr
@@ -114,6 +201,7 @@ def _params(steps: int, eps: float, coefficients, precision: int):
 
 def _run(name: str, table: _Table, workspace, workspace_bytes: int, steps, eps, coefficients, precision, stream) -> None:
     p, keep = _params(steps, eps, coefficients, precision)
+    _check_device(table.device)
     st = getattr(_native.lib(), name)(table.ptr, len(table), ctypes.byref(p), _addr(workspace) or None, int(workspace_bytes),
                                       stream_handle(stream))
     if st:

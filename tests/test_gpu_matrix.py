@@ -590,3 +590,27 @@ def test_auto_precision_is_full_for_bf16_results():
         share = 3 * tolerance(r, c, True, False) * np.linalg.norm(want) / math.sqrt(want.size)
         off = np.abs(x - rounded)
         assert np.all(off <= 2.0**-7 * np.abs(want) + share)
+
+
+def test_tables_take_type_and_stride_from_tensors():
+    """BF16 tensors and column slices given without codes and strides."""
+    T = torch()
+    log("tables from tensors")
+    src = T.from_numpy(matrix(70, 90, 5)).cuda()
+    wide = T.full((70, 101), 9.0, device="cuda").bfloat16()
+    wide[:, :90] = src
+    out = T.full((70, 95), 7.0, device="cuda").bfloat16()
+    table = lso.MatrixTable.from_rows([dict(x=wide[:, :90], y=out[:, :90], rows=70, cols=90)])
+    assert table.arr[["ld_x", "ld_y", "x_dtype", "y_dtype"]].tolist() == [(101, 95, 2, 2)]
+    need = lso.orthogonalize_workspace_bytes(table)
+    lso.orthogonalize(table, workspace(need), need)
+    T.cuda.synchronize()
+    check(out[:, :90].float().cpu().numpy(), ortho64(wide[:, :90].float().cpu().numpy()), 70, 90, True, True, "slices")
+    assert bool((out[:, 90:] == 7.0).all())
+    b = Block([(70, 90)], "f32", True, seed=6)
+    b.table = lso.MuonTable.from_rows([dict(rows=70, cols=90, master=b.master[:-1].view(70, 90), m=b.m[:-1], grad=b.grad[:-1].view(70, 90),
+                                            weight=b.w[:-1])])
+    assert b.table.arr["grad_dtype"].tolist() == [1]
+    log("update from tensors")
+    run_muon(b)
+    b.check(what="from tensors")

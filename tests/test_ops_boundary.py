@@ -261,3 +261,52 @@ def test_half_precision_is_the_callers_choice():
         tab = lso.MatrixTable.from_rows([mat(x_dtype=lso.LSO_DT_BF16, y_dtype=y_dtype), mat(1, x_dtype=lso.LSO_DT_BF16, y_dtype=y_dtype)])
         full, half = (lso.orthogonalize_workspace_bytes(tab, p) for p in (lso.LSO_NS_FULL, lso.LSO_NS_HALF))
         assert lso.orthogonalize_workspace_bytes(tab) == full > half
+
+
+def test_matrix_tables_look_at_tensors():
+    """Tensors whose type, shape, strides or place contradict the row are
+    refused (CPU tensors here: what is not wrong otherwise fails on that)."""
+    import torch
+    f, h = torch.zeros(6, 10), torch.zeros(6, 10, dtype=torch.bfloat16)
+
+    def refused(error, match, **kw):
+        row = dict(x=f, y=A, rows=6, cols=10)
+        row.update(kw)
+        with pytest.raises(error, match=match):
+            lso.MatrixTable.from_rows([row])
+        tab = lso.MatrixTable(1)
+        with pytest.raises(error, match=match):
+            tab.set_row(0, **row)
+        assert tab.arr[0]["rows"] == 0
+
+    refused(TypeError, "y: ", y=h, y_dtype=1)
+    refused(TypeError, "x: ", x=f, x_dtype=2)
+    refused(TypeError, "float16", x=f.half())
+    refused(TypeError, "x: .*int32", x=f.int())
+    refused(TypeError, "x: .*int16", x=f.short(), x_dtype=1)
+    refused(ValueError, "contiguous", x=torch.zeros(10, 6).T)
+    refused(ValueError, "row stride 10 given", x=torch.zeros(6, 12)[:, :10], ld_x=10)
+    refused(ValueError, "does not hold", x=f[:5])
+    refused(ValueError, "does not hold", x=f, ld_x=11, rows=6, cols=9)
+    refused(ValueError, "does not hold", x=torch.zeros(120)[::2])
+    for x, kw in ((f, {}), (f.flatten(), {}), (torch.zeros(6, 12)[:, :10], {}), (torch.zeros(72), dict(ld_x=12)), (h, {}),
+                  (f.int(), dict(x_dtype=1)), (f.short(), dict(x_dtype=2))):
+        refused(ValueError, "not on a GPU", x=x, **kw)
+    assert ops._array(h, "x", None, 1, 6, 10) == (h.data_ptr(), 2, 10)
+    assert ops._array(torch.zeros(6, 12)[:, :10], "x", None, 2, 6, 10)[1:] == (1, 12)
+    assert ops._array(torch.zeros(72), "x", 1, 2, 6, 10, 12)[1:] == (1, 12)
+    assert ops._array(A, "x", None, 2, 6, 10) == (A, 2, 10) and ops._array(None, "x", None, 1, 6, 10) == (0, 1, 10)
+
+
+def test_muon_tables_look_at_tensors():
+    import torch
+    f = torch.zeros(64, 96)
+    for error, match, kw in ((TypeError, "grad: ", dict(grad=f, grad_dtype=2)), (TypeError, "float64", dict(grad=f.double())),
+                             (TypeError, "master: ", dict(master=f.bfloat16())), (TypeError, "weight: ", dict(weight=f)),
+                             (ValueError, "m must be contiguous", dict(m=torch.zeros(64, 100)[:, :96])),
+                             (ValueError, "grad: .*row must be contiguous", dict(grad=torch.zeros(96, 64).T)),
+                             (ValueError, "weight: .*does not hold", dict(weight=f[:63].bfloat16())),
+                             (ValueError, "offsets", dict(base=A, grad=f)), (ValueError, "grad is on cpu", dict(grad=f))):
+        with pytest.raises(error, match=match):
+            lso.MuonTable.from_rows([block(**kw)])
+    assert lso.MuonTable.from_rows([block()]).arr["grad_dtype"].tolist() == [2]
