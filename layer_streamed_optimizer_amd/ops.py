@@ -185,6 +185,17 @@ class MuonTable(_Table):
         self.arr["lr"] = lr
 
 
+def _workspace(workspace, nbytes: int) -> int | None:
+    """The address of a workspace; a torch tensor has to hold nbytes on the
+    current device."""
+    if workspace is None or isinstance(workspace, int):
+        return workspace or None
+    _check_device(_gpu(workspace, "the workspace"))
+    if not workspace.is_contiguous() or workspace.nbytes < nbytes:
+        raise ValueError(f"the workspace tensor holds {workspace.nbytes} contiguous bytes, not the {nbytes} given")
+    return workspace.data_ptr() or None
+
+
 def _params(steps: int, eps: float, coefficients, precision: int):
     """lso_ns_params and the array it points into (to be kept alive)."""
     coef = None
@@ -202,7 +213,7 @@ def _params(steps: int, eps: float, coefficients, precision: int):
 def _run(name: str, table: _Table, workspace, workspace_bytes: int, steps, eps, coefficients, precision, stream) -> None:
     p, keep = _params(steps, eps, coefficients, precision)
     _check_device(table.device)
-    st = getattr(_native.lib(), name)(table.ptr, len(table), ctypes.byref(p), _addr(workspace) or None, int(workspace_bytes),
+    st = getattr(_native.lib(), name)(table.ptr, len(table), ctypes.byref(p), _workspace(workspace, workspace_bytes), int(workspace_bytes),
                                       stream_handle(stream))
     if st:
         _native.check(st, name)
@@ -294,7 +305,7 @@ def embed_grad(tokens, dy, grad, workspace, workspace_bytes: int, *, scale: floa
     """grad[v] = scale * sum of dy[i] over the positions i of token v (+= with
     accumulate), every row of grad written.  Torch tensors; asynchronous."""
     e = _embed(tokens, grad, dy, scale, LSO_EMBED_ADD if accumulate else 0)
-    st = _native.lib().lso_embed_grad(ctypes.byref(e), _addr(workspace) or None, int(workspace_bytes), stream_handle(stream))
+    st = _native.lib().lso_embed_grad(ctypes.byref(e), _workspace(workspace, workspace_bytes), int(workspace_bytes), stream_handle(stream))
     if st:
         _native.check(st, "lso_embed_grad")
 
@@ -318,7 +329,7 @@ class EmbedProducer:
         self._grad_dtype, self._scale = grad_dtype, scale
         a = self._args
         a.embed_layer = embed_layer
-        a.workspace, a.workspace_bytes = _addr(workspace) or None, int(workspace_bytes)
+        a.workspace, a.workspace_bytes = _workspace(workspace, workspace_bytes), int(workspace_bytes)
         a.other, a.other_user = other or None, other_user or None
         self.set_batch(tokens, dy)
         self.fn = ctypes.cast(_native.lib().lso_embed_producer, ctypes.c_void_p).value

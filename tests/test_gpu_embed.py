@@ -343,3 +343,16 @@ def test_producer_in_the_layer_stream(grad_dt):
     ls.close()
     for hb in bufs:
         hb.close()
+
+
+def test_gradient_refuses_a_workspace_tensor_that_is_too_small():
+    """(Refused before anything is enqueued.)"""
+    T = torch()
+    t, dy, grad = T.zeros(100, dtype=T.int64, device="cuda"), T.zeros(100, 16, device="cuda"), T.full((8, 16), 3.0, device="cuda")
+    need = lso.embed_grad_workspace_bytes(100, 8, 16)
+    log("gradient with workspaces that are refused")
+    for ws in (T.empty(need - 1, dtype=T.uint8, device="cuda"), T.empty(need, dtype=T.uint8), T.empty(2 * need, dtype=T.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            lso.embed_grad(t, dy, grad, ws, need)
+    T.cuda.synchronize()
+    assert bool((grad == 3.0).all())

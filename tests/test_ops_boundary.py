@@ -310,3 +310,21 @@ def test_muon_tables_look_at_tensors():
         with pytest.raises(error, match=match):
             lso.MuonTable.from_rows([block(**kw)])
     assert lso.MuonTable.from_rows([block()]).arr["grad_dtype"].tolist() == [2]
+
+
+def test_workspace_tensors_are_looked_at(monkeypatch):
+    """A workspace tensor that is not on a GPU, or holds less than is said."""
+    import torch
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    tables = lso.MatrixTable.from_rows([mat()]), lso.MuonTable.from_rows([block()])
+    for call in (lambda w, n: lso.orthogonalize(tables[0], w, n, stream=0), lambda w, n: lso.muon_step(tables[1], w, n, stream=0)):
+        with pytest.raises(ValueError, match="workspace is on cpu"):
+            call(ws, 1 << 20)
+    with monkeypatch.context() as patch:
+        patch.setattr(ops, "_gpu", lambda x, name: None)     # as if it were on the current GPU
+        for call in (lambda w, n: lso.orthogonalize(tables[0], w, n, stream=0), lambda w, n: lso.muon_step(tables[1], w, n, stream=0)):
+            for w in (ws, ws[::2], torch.zeros(1 << 18, dtype=torch.int16)):
+                with pytest.raises(ValueError, match="holds"):
+                    call(w, (1 << 20) + 1 if w is ws else 1 << 19 if w.dtype == torch.uint8 else (1 << 19) + 1)
+        assert ops._workspace(ws, 1 << 20) == ws.data_ptr()
+    assert ops._workspace(WS, BIG) == WS and ops._workspace(None, 0) is None and ops._workspace(0, 0) is None
