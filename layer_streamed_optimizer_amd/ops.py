@@ -185,12 +185,16 @@ class MuonTable(_Table):
         self.arr["lr"] = lr
 
 
-def _workspace(workspace, nbytes: int) -> int | None:
+def _workspace(workspace, nbytes: int, device: int | None = None) -> int | None:
     """The address of a workspace; a torch tensor has to hold nbytes on the
-    current device."""
+    current device (or on the one given)."""
     if workspace is None or isinstance(workspace, int):
         return workspace or None
-    _check_device(_gpu(workspace, "the workspace"))
+    at = _gpu(workspace, "the workspace")
+    if device is None:
+        _check_device(at)
+    elif at != device:
+        raise ValueError(f"the workspace is on GPU {at}, the tokens on GPU {device}")
     if not workspace.is_contiguous() or workspace.nbytes < nbytes:
         raise ValueError(f"the workspace tensor holds {workspace.nbytes} contiguous bytes, not the {nbytes} given")
     return workspace.data_ptr() or None
@@ -319,8 +323,9 @@ class EmbedProducer:
 
     grad_dtype is the embedding layer's (LSO_DT_BF16 or LSO_DT_F32); other:
     the producer of the other layers (a C function pointer, called with
-    other_user).  The tensors and this object must live as long as the
-    stream uses them; set_batch takes the next batch's."""
+    other_user).  The tensors are on the stream's GPU; they and this object
+    must live as long as the stream uses them; set_batch takes the next
+    batch's."""
 
     def __init__(self, tokens, dy, vocab: int, width: int, workspace, workspace_bytes: int, *, embed_layer: int = 0,
                  grad_dtype: int = LSO_DT_BF16, scale: float = 1.0, other: int = 0, other_user: int = 0):
@@ -329,9 +334,11 @@ class EmbedProducer:
         self._grad_dtype, self._scale = grad_dtype, scale
         a = self._args
         a.embed_layer = embed_layer
-        a.workspace, a.workspace_bytes = _workspace(workspace, workspace_bytes), int(workspace_bytes)
         a.other, a.other_user = other or None, other_user or None
+        self._device = _gpu(tokens, "tokens")
         self.set_batch(tokens, dy)
+        a.workspace, a.workspace_bytes = _workspace(workspace, workspace_bytes, self._device), int(workspace_bytes)
+        self._workspace = workspace
         self.fn = ctypes.cast(_native.lib().lso_embed_producer, ctypes.c_void_p).value
         self.user = ctypes.addressof(a)
 
@@ -341,6 +348,8 @@ class EmbedProducer:
             raise ValueError("tokens must be contiguous and dy [tokens, width]")
         if dy.shape[0] > 0 and width > 1 and dy.stride(1) != 1:
             raise ValueError("dy: the elements of a row must be contiguous")
+        if _gpu(tokens, "tokens") != self._device or _gpu(dy, "dy") != self._device:
+            raise ValueError(f"tokens and dy must be on GPU {self._device}, where the first batch was")
         e = self._args.grad
         e.tokens, e.n, e.token_dtype = tokens.data_ptr() or None, tokens.numel(), dtype_of(tokens)
         e.rows, e.rows_dtype = dy.data_ptr() or None, dtype_of(dy)

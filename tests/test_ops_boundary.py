@@ -328,3 +328,30 @@ def test_workspace_tensors_are_looked_at(monkeypatch):
                     call(w, (1 << 20) + 1 if w is ws else 1 << 19 if w.dtype == torch.uint8 else (1 << 19) + 1)
         assert ops._workspace(ws, 1 << 20) == ws.data_ptr()
     assert ops._workspace(WS, BIG) == WS and ops._workspace(None, 0) is None and ops._workspace(0, 0) is None
+
+
+def test_embedding_producer_looks_at_tensors(monkeypatch):
+    """Tensors that are not on a GPU, or not all on one, are refused when the
+    producer is made or given a batch, before a stream could run it."""
+    import torch
+    t, dy, ws = torch.zeros(3, dtype=torch.int64), torch.zeros(3, 8), torch.zeros(64, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="tokens is on cpu"):
+        lso.EmbedProducer(t, dy, 5, 8, WS, BIG)
+    places = {id(t): 0, id(dy): 0, id(ws): 0}
+    monkeypatch.setattr(ops, "_gpu", lambda x, name: places[id(x)])
+    p = lso.EmbedProducer(t, dy, 5, 8, ws, 64)
+    assert p._args.workspace == ws.data_ptr() and p._args.grad.tokens == t.data_ptr()
+    with pytest.raises(ValueError, match="holds"):
+        lso.EmbedProducer(t, dy, 5, 8, ws, 65)
+    places[id(ws)] = 1
+    with pytest.raises(ValueError, match="workspace is on GPU 1"):
+        lso.EmbedProducer(t, dy, 5, 8, ws, 64)
+    for x in (t, dy):
+        places[id(x)] = 1
+        with pytest.raises(ValueError, match="must be on GPU 0"):
+            p.set_batch(t, dy)
+        places[id(x)] = 0
+    p.set_batch(t, dy)
+    monkeypatch.undo()
+    with pytest.raises(ValueError, match="is on cpu"):
+        p.set_batch(t, dy)
