@@ -190,7 +190,9 @@ lso_status lso_embed_grad(const lso_embed* e, void* workspace, uint64_t workspac
  * and ld_table of `grad` are replaced, table_dtype must be the layer's
  * grad_dtype, LSO_EMBED_ADD is refused), for every other layer it calls
  * `other` with `other_user`.  Pass lso_embed_producer as the function and a
- * lso_embed_producer_args as its user pointer. */
+ * lso_embed_producer_args as its user pointer.  A layer stream's own streams
+ * wait for no other stream: tokens and rows must be complete on the device
+ * when lso_stream_layers or lso_stream_files is called. */
 typedef struct lso_embed_producer_args {
     lso_embed   grad;
     size_t      embed_layer;

@@ -324,8 +324,10 @@ class EmbedProducer:
     grad_dtype is the embedding layer's (LSO_DT_BF16 or LSO_DT_F32); other:
     the producer of the other layers (a C function pointer, called with
     other_user).  The tensors are on the stream's GPU; they and this object
-    must live as long as the stream uses them; set_batch takes the next
-    batch's."""
+    must live as long as the stream uses them.  A layer stream's own streams
+    wait for no other: set_batch, which takes the next batch's tensors,
+    returns when the work of torch's current stream so far is done, and
+    whoever refills the same tensors calls it again."""
 
     def __init__(self, tokens, dy, vocab: int, width: int, workspace, workspace_bytes: int, *, embed_layer: int = 0,
                  grad_dtype: int = LSO_DT_BF16, scale: float = 1.0, other: int = 0, other_user: int = 0):
@@ -357,3 +359,6 @@ class EmbedProducer:
         e.vocab, e.width, e.ld_table, e.table_dtype = vocab, width, width, self._grad_dtype
         e.scale = self._scale
         self._keep = (tokens, dy)
+        if self._device is not None:
+            import torch
+            torch.cuda.current_stream(self._device).synchronize()

@@ -356,3 +356,42 @@ def test_gradient_refuses_a_workspace_tensor_that_is_too_small():
             lso.embed_grad(t, dy, grad, ws, need)
     T.cuda.synchronize()
     assert bool((grad == 3.0).all())
+
+
+def test_producer_waits_for_the_batch_it_is_given():
+    """A batch that is still being written when the producer gets it: the layer
+    stream's update uses what it ends as."""
+    from layer_streamed_optimizer_amd import configs
+    T = torch()
+    n, vocab, width = 300, 50, 64
+    om, omm, ov, nbytes = configs.host_layer_layout(vocab * width)
+    t = T.from_numpy(tokens(n, vocab, 3)).cuda()
+    first, dy = T.ones(n, width, device="cuda"), T.zeros(n, width, device="cuda")
+    need = lso.embed_grad_workspace_bytes(n, vocab, width)
+    ws = workspace(need)
+    p = lso.EmbedProducer(t, first, vocab, width, ws, need, grad_dtype=lso.LSO_DT_F32)
+    ls = lso.LayerStream(nbytes, vocab * width, p.fn, p.user)
+    hb = lso.host_alloc(nbytes)
+    hb.view(np.uint8)[:] = 0
+    L = lso.LayerStream.layers(1)
+    L[0]["host_base"], L[0]["bytes"], L[0]["n"] = hb.ptr, nbytes, vocab * width
+    L[0]["off_master"], L[0]["off_m"], L[0]["off_v"] = om, omm, ov
+    L[0]["t"], L[0]["lr"], L[0]["beta1"], L[0]["beta2"], L[0]["eps"] = 1, 1e-2, 0.9, 0.999, 1e-8
+    L[0]["grad_dtype"] = lso.LSO_DT_F32
+    a = T.randn(4096, 4096, device="cuda")
+    T.cuda.synchronize()
+    log("producer with a batch that is being written")
+    with T.cuda.stream(T.cuda.Stream()):
+        for _ in range(8):
+            a = a @ a * 1e-2                 # some milliseconds of work before the batch is there
+        dy.fill_(2.0)
+        p.set_batch(t, dy)
+        ls.stream_layers(L)
+    want = np.zeros(vocab)
+    host = t.cpu().numpy()
+    np.add.at(want, host[(host >= 0) & (host < vocab)], 2.0)
+    m = hb.view(np.float32, omm, vocab * width).reshape(vocab, width).astype(np.float64)
+    # m' = (1 - beta1) g: g is exact, the constant and the product are rounded
+    assert np.all(np.abs(m - 0.1 * want[:, None]) <= 2.001 * 2.0**-24 * 0.1 * want[:, None])
+    ls.close()
+    hb.close()

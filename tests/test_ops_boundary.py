@@ -5,6 +5,7 @@ import ctypes
 import os
 import re
 import subprocess
+from unittest import mock
 
 import numpy as np
 import pytest
@@ -339,6 +340,7 @@ def test_embedding_producer_looks_at_tensors(monkeypatch):
         lso.EmbedProducer(t, dy, 5, 8, WS, BIG)
     places = {id(t): 0, id(dy): 0, id(ws): 0}
     monkeypatch.setattr(ops, "_gpu", lambda x, name: places[id(x)])
+    monkeypatch.setattr(torch.cuda, "current_stream", mock.Mock())
     p = lso.EmbedProducer(t, dy, 5, 8, ws, 64)
     assert p._args.workspace == ws.data_ptr() and p._args.grad.tokens == t.data_ptr()
     with pytest.raises(ValueError, match="holds"):
@@ -355,3 +357,23 @@ def test_embedding_producer_looks_at_tensors(monkeypatch):
     monkeypatch.undo()
     with pytest.raises(ValueError, match="is on cpu"):
         p.set_batch(t, dy)
+
+
+def test_embedding_producer_waits_for_its_tensors(monkeypatch):
+    """The layer stream's streams wait for no other, so the producer waits for
+    the work that writes its batch."""
+    import torch
+    t, dy, seen = torch.zeros(3, dtype=torch.int64), torch.zeros(3, 8), []
+
+    class Stream:
+        def __init__(self, device):
+            self.device = device
+
+        def synchronize(self):
+            seen.append(self.device)
+    monkeypatch.setattr(ops, "_gpu", lambda x, name: 2)
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    p = lso.EmbedProducer(t, dy, 5, 8, WS, BIG)
+    assert seen == [2]
+    p.set_batch(t, dy)
+    assert seen == [2, 2]
