@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "lso_bf16.h"
+#include "lso_launch.h"
 #include "lso_ops.h"
 #include "lso_runtime.h"
 
@@ -627,46 +628,41 @@ lso_status launch_lookup(const lso_embed& e, hipStream_t s)
     if (groups > kMaxGroups) return too_large();
     const dim3 grid(static_cast<uint32_t>(groups)), threads(256);
     const bool t32 = e.table_dtype == LSO_DT_F32, r32 = e.rows_dtype == LSO_DT_F32;
-    auto launch = [&](auto once) {
+    auto enqueue = [&](auto once) {
         constexpr bool kOnce = decltype(once)::value;
-        if (t32 && r32) hipLaunchKernelGGL((embed_lookup_kernel<V, true, true, kOnce>), grid, threads, 0, s, a);
-        else if (t32) hipLaunchKernelGGL((embed_lookup_kernel<V, true, false, kOnce>), grid, threads, 0, s, a);
-        else if (r32) hipLaunchKernelGGL((embed_lookup_kernel<V, false, true, kOnce>), grid, threads, 0, s, a);
-        else hipLaunchKernelGGL((embed_lookup_kernel<V, false, false, kOnce>), grid, threads, 0, s, a);
+        const auto kernel = t32 ? (r32 ? embed_lookup_kernel<V, true, true, kOnce> : embed_lookup_kernel<V, true, false, kOnce>)
+                                : (r32 ? embed_lookup_kernel<V, false, true, kOnce> : embed_lookup_kernel<V, false, false, kOnce>);
+        return launch(kernel, grid, threads, s, a);
     };
-    if (beyond_l2(e)) launch(std::true_type{});
-    else launch(std::false_type{});
-    const hipError_t err = hipGetLastError();
+    const hipError_t err = beyond_l2(e) ? enqueue(std::true_type{}) : enqueue(std::false_type{});
     return err == hipSuccess ? LSO_OK : hip_fail(err, "embedding lookup launch");
 }
 
 template <int V, bool kRowsF32, bool kTableF32>
-void launch_grad_typed(const GradArgs& a, bool once, hipStream_t s)
+hipError_t launch_grad_typed(const GradArgs& a, bool once, hipStream_t s)
 {
     const dim3 threads(256);
     const uint32_t rows_per_wave = rows_of_wave(a.n, a.vocab), row_groups = (a.vocab + 4 * rows_per_wave - 1) / (4 * rows_per_wave);
     const uint32_t blocks = a.n > kRun ? (a.n + kRun - 1) / kRun : 0;   // a run of up to kRun is no long one
     const uint32_t chunks = (a.width + 64 * V - 1) / (64 * V);
     const uint32_t jobs = blocks * chunks, part_groups = (jobs + 3) / 4;
-    const dim3 grid(part_groups + row_groups);
-    if (once)
-        hipLaunchKernelGGL((embed_grad_kernel<V, kRowsF32, kTableF32, true>), grid, threads, 0, s, a, part_groups, chunks, rows_per_wave);
-    else
-        hipLaunchKernelGGL((embed_grad_kernel<V, kRowsF32, kTableF32, false>), grid, threads, 0, s, a, part_groups, chunks, rows_per_wave);
-    if (blocks > 0) hipLaunchKernelGGL((embed_grad_join_kernel<V, kTableF32>), dim3(jobs), threads, 0, s, a, chunks);
+    const auto kernel = once ? embed_grad_kernel<V, kRowsF32, kTableF32, true> : embed_grad_kernel<V, kRowsF32, kTableF32, false>;
+    hipError_t err = launch(kernel, dim3(part_groups + row_groups), threads, s, a, part_groups, chunks, rows_per_wave);
+    if (err == hipSuccess && blocks > 0) err = launch(embed_grad_join_kernel<V, kTableF32>, dim3(jobs), threads, s, a, chunks);
+    return err;
 }
 
 template <int V>
-void launch_grad(const GradArgs& a, bool r32, bool t32, bool once, hipStream_t s)
+hipError_t launch_grad(const GradArgs& a, bool r32, bool t32, bool once, hipStream_t s)
 {
-    if (r32 && t32) launch_grad_typed<V, true, true>(a, once, s);
-    else if (r32) launch_grad_typed<V, true, false>(a, once, s);
-    else if (t32) launch_grad_typed<V, false, true>(a, once, s);
-    else launch_grad_typed<V, false, false>(a, once, s);
+    if (r32 && t32) return launch_grad_typed<V, true, true>(a, once, s);
+    if (r32) return launch_grad_typed<V, true, false>(a, once, s);
+    if (t32) return launch_grad_typed<V, false, true>(a, once, s);
+    return launch_grad_typed<V, false, false>(a, once, s);
 }
 
 // Sort the tokens into workspace; sets a.keys and a.pos.
-void launch_sort(const lso_embed& e, char* work, const GradWork& w, GradArgs& a, hipStream_t s)
+hipError_t launch_sort(const lso_embed& e, char* work, const GradWork& w, GradArgs& a, hipStream_t s)
 {
     uint32_t bits = 1;
     while ((e.vocab >> bits) != 0) ++bits;   // the largest key is vocab
@@ -675,10 +671,9 @@ void launch_sort(const lso_embed& e, char* work, const GradWork& w, GradArgs& a,
         x.tokens = tokens_of(e);
         x.keys_out = reinterpret_cast<uint32_t*>(work + w.keys[0]);
         x.pos_out = reinterpret_cast<uint32_t*>(work + w.pos[0]);
-        hipLaunchKernelGGL(sort_by_rank_kernel, dim3((x.tokens.n + 63) / 64), dim3(1024), 0, s, x);
         a.keys = x.keys_out;
         a.pos = x.pos_out;
-        return;
+        return launch(sort_by_rank_kernel, dim3((x.tokens.n + 63) / 64), dim3(1024), s, x);
     }
     const uint32_t passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
     SortArgs x{};
@@ -689,18 +684,20 @@ void launch_sort(const lso_embed& e, char* work, const GradWork& w, GradArgs& a,
         x.tile = static_cast<uint32_t>(((e.n + kMaxSortGroups - 1) / kMaxSortGroups + kSortThreads - 1) / kSortThreads * kSortThreads);
     x.groups = static_cast<uint32_t>((e.n + x.tile - 1) / x.tile);
     x.bits = (bits + passes - 1) / passes;
-    for (uint32_t p = 0; p < passes; ++p) {
+    hipError_t err = hipSuccess;
+    for (uint32_t p = 0; p < passes && err == hipSuccess; ++p) {
         x.first = p == 0;
         x.shift = p * x.bits;
         x.keys = reinterpret_cast<const uint32_t*>(work + w.keys[(p + 1) & 1u]);
         x.pos = reinterpret_cast<const uint32_t*>(work + w.pos[(p + 1) & 1u]);
         x.keys_out = reinterpret_cast<uint32_t*>(work + w.keys[p & 1u]);
         x.pos_out = reinterpret_cast<uint32_t*>(work + w.pos[p & 1u]);
-        hipLaunchKernelGGL(sort_count_kernel, dim3(x.groups), dim3(kSortThreads), 0, s, x);
-        hipLaunchKernelGGL(sort_scatter_kernel, dim3(x.groups), dim3(kSortThreads), 0, s, x);
+        err = launch(sort_count_kernel, dim3(x.groups), dim3(kSortThreads), s, x);
+        if (err == hipSuccess) err = launch(sort_scatter_kernel, dim3(x.groups), dim3(kSortThreads), s, x);
     }
     a.keys = x.keys_out;
     a.pos = x.pos_out;
+    return err;
 }
 
 lso_status lookup(const lso_embed* e, void* stream)
@@ -713,7 +710,6 @@ lso_status lookup(const lso_embed* e, void* stream)
     st = check_overlap(iv);
     if (st != LSO_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    (void)hipGetLastError();   // an error left by other work is not this call's
     return vectors(*e) ? launch_lookup<8>(*e, s) : launch_lookup<1>(*e, s);
 }
 
@@ -740,7 +736,6 @@ lso_status gradient(const lso_embed* e, void* workspace, uint64_t workspace_byte
     const uint64_t columns = (e->width + (vec ? 511 : 63)) / (vec ? 512 : 64);   // column runs of a wave
     if (e->vocab / (4 * rows_of_wave(e->n, e->vocab)) + 1 + (e->n + kRun - 1) / kRun * columns > kMaxGroups) return too_large();
     hipStream_t s = static_cast<hipStream_t>(stream);
-    (void)hipGetLastError();   // an error left by other work is not this call's
     char* work = static_cast<char*>(workspace);
     GradArgs a{};
     a.rows = e->rows;
@@ -753,11 +748,9 @@ lso_status gradient(const lso_embed* e, void* workspace, uint64_t workspace_byte
     a.width = static_cast<uint32_t>(e->width);
     a.scale = static_cast<float>(e->scale);
     a.add = (e->flags & LSO_EMBED_ADD) != 0;
-    if (e->n > 0) launch_sort(*e, work, w, a, s);
+    hipError_t err = e->n > 0 ? launch_sort(*e, work, w, a, s) : hipSuccess;
     const bool r32 = e->rows_dtype == LSO_DT_F32, t32 = e->table_dtype == LSO_DT_F32;
-    if (vec) launch_grad<8>(a, r32, t32, beyond_l2(*e), s);
-    else launch_grad<1>(a, r32, t32, false, s);
-    const hipError_t err = hipGetLastError();
+    if (err == hipSuccess) err = vec ? launch_grad<8>(a, r32, t32, beyond_l2(*e), s) : launch_grad<1>(a, r32, t32, false, s);
     return err == hipSuccess ? LSO_OK : hip_fail(err, "embedding gradient launch");
 }
 

@@ -22,6 +22,7 @@
 #include <cstdint>
 
 #include "lso_bf16.h"
+#include "lso_launch.h"
 #include "lso_ns.h"
 
 namespace lso {
@@ -59,14 +60,14 @@ __global__ void __launch_bounds__(64) ns_table_kernel(const NsTablePart<kCount> 
 }
 
 template <uint32_t kCount>
-void write_table(NsMat* dst, const NsMat* src, uint32_t count, hipStream_t s)
+hipError_t write_table(NsMat* dst, const NsMat* src, uint32_t count, hipStream_t s)
 {
     NsTablePart<kCount> part;
     part.dst = dst;
     part.count = count;
     part.pad = 0;
     for (uint32_t j = 0; j < kCount; ++j) part.src[j] = src[j < count ? j : 0];
-    hipLaunchKernelGGL(ns_table_kernel<kCount>, dim3((count + 63) / 64), dim3(64), 0, s, part);
+    return launch(ns_table_kernel<kCount>, dim3((count + 63) / 64), dim3(64), s, part);
 }
 
 __device__ __forceinline__ NsMat load_mat(const NsMat* tab, uint32_t i)
@@ -1207,10 +1208,10 @@ hipError_t launch_small(const NsCall& c, const NsMat* tab, uint32_t n, uint32_t 
     args.steps = c.steps;
     args.eps = c.eps;
     for (uint32_t k = 0; k < 3 * c.steps; ++k) args.coef[k] = c.coef[k];
-    hipLaunchKernelGGL(ns_small_gram_kernel<kK>, dim3(chunks), dim3(256), 0, s, tab, n, index);
-    hipLaunchKernelGGL(ns_small_iterate_kernel<kK>, dim3(n), dim3(small_threads(kK)), 0, s, args);
-    hipLaunchKernelGGL(ns_small_apply_kernel<kK>, dim3(chunks), dim3(256), 0, s, tab, n, index);
-    return hipGetLastError();
+    hipError_t err = launch(ns_small_gram_kernel<kK>, dim3(chunks), dim3(256), s, tab, n, index);
+    if (err == hipSuccess) err = launch(ns_small_iterate_kernel<kK>, dim3(n), dim3(small_threads(kK)), s, args);
+    if (err == hipSuccess) err = launch(ns_small_apply_kernel<kK>, dim3(chunks), dim3(256), s, tab, n, index);
+    return err;
 }
 
 // The general path.  kTerms: of X as S reads it, and of what X is multiplied by.
@@ -1229,11 +1230,11 @@ public:
     hipError_t run()
     {
         const NsMat* tab = args_.tab;
-        hipLaunchKernelGGL(ns_norm_kernel, dim3(c_.prep_tiles), dim3(256), 0, s_, tab, c_.nbig, c_.prep_index, c_.layout, c_.counters, c_.ncounters);
-        hipLaunchKernelGGL(ns_scale_kernel, dim3(c_.nbig), dim3(1024), 0, s_, tab, c_.layout, c_.eps);
-        if (xt_terms(0) == 2) hipLaunchKernelGGL((ns_split_kernel<kT, kTerms, 2>), dim3(c_.prep_tiles), dim3(256), 0, s_, tab, c_.nbig, c_.prep_index, c_.layout);
-        else hipLaunchKernelGGL((ns_split_kernel<kT, kTerms, 1>), dim3(c_.prep_tiles), dim3(256), 0, s_, tab, c_.nbig, c_.prep_index, c_.layout);
-        for (uint32_t k = 0; k < c_.steps;) {
+        enqueue(ns_norm_kernel, c_.prep_tiles, 256, tab, c_.nbig, c_.prep_index, c_.layout, c_.counters, c_.ncounters);
+        enqueue(ns_scale_kernel, c_.nbig, 1024, tab, c_.layout, c_.eps);
+        enqueue(xt_terms(0) == 2 ? ns_split_kernel<kT, kTerms, 2> : ns_split_kernel<kT, kTerms, 1>, c_.prep_tiles, 256, tab, c_.nbig,
+                c_.prep_index, c_.layout);
+        for (uint32_t k = 0; k < c_.steps && err_ == hipSuccess;) {
             const bool pair = paired(k);
             gram();
             poly(k, 0, 1, !pair);
@@ -1246,10 +1247,17 @@ public:
             apply(k, pair ? k + 2 : k + 1, pair ? 2 : 1);
             k += pair ? 2 : 1;
         }
-        return hipGetLastError();
+        return err_;
     }
 
 private:
+    // Nothing more is enqueued after an error.
+    template <typename... P>
+    void enqueue(void (*kernel)(P...), uint32_t groups, uint32_t threads, const typename as_is<P>::type&... args)
+    {
+        if (err_ == hipSuccess) err_ = lso::launch(kernel, dim3(groups), dim3(threads), s_, args...);
+    }
+
     bool paired(uint32_t k) const { return c_.pairs && c_.pair[k]; }
 
     // Terms of X^T where step k reads it.  In half precision the last two
@@ -1262,7 +1270,7 @@ private:
     {
         args_.depth = p.depth;
         args_.index = p.index;
-        hipLaunchKernelGGL((ns_product_kernel<kT, kA, kB, kKind, kOut>), dim3(p.units), dim3(kT == 256 ? 512 : 256), 0, s_, args_);
+        enqueue(ns_product_kernel<kT, kA, kB, kKind, kOut>, p.units, kT == 256 ? 512 : 256, args_);
     }
 
     bool two_term_squares() const { return c_.layout.square_terms == 2; }
@@ -1325,6 +1333,7 @@ private:
 
     const NsCall& c_;
     hipStream_t s_;
+    hipError_t err_ = hipSuccess;
     ProductArgs args_{};
 };
 
@@ -1339,14 +1348,13 @@ hipError_t launch_big(const NsCall& c, const NsMat* tab, hipStream_t s)
 int ns_launch(const NsCall& c, NsMat* device_table, void* stream)
 {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    (void)hipGetLastError();   // an error left by other work is not this call's
     uint32_t total = c.nbig;
     for (int k = 0; k < kNsClasses; ++k) total += c.nsmall[k];
-    for (uint32_t k = 0; k < total; k += kWriteMany) {
-        if (total - k <= kWriteFew) write_table<kWriteFew>(device_table + k, c.table + k, total - k, s);
-        else write_table<kWriteMany>(device_table + k, c.table + k, total - k < kWriteMany ? total - k : kWriteMany, s);
+    hipError_t err = hipSuccess;
+    for (uint32_t k = 0; k < total && err == hipSuccess; k += kWriteMany) {
+        if (total - k <= kWriteFew) err = write_table<kWriteFew>(device_table + k, c.table + k, total - k, s);
+        else err = write_table<kWriteMany>(device_table + k, c.table + k, total - k < kWriteMany ? total - k : kWriteMany, s);
     }
-    hipError_t err = hipGetLastError();
     const NsMat* tab = device_table;
     for (int k = 0; k < kNsClasses && err == hipSuccess; ++k) {
         if (c.nsmall[k] == 0) continue;

@@ -395,3 +395,34 @@ def test_producer_waits_for_the_batch_it_is_given():
     assert np.all(np.abs(m - 0.1 * want[:, None]) <= 2.001 * 2.0**-24 * 0.1 * want[:, None])
     ls.close()
     hb.close()
+
+
+def test_an_error_left_by_other_work_stays_there():
+    """An error that other code of the thread has not collected: the calls
+    neither report it nor take it away."""
+    from test_gpu_matrix import Block, Mats
+    T, lib = torch(), _native.lib()
+    n, vocab, width = 5000, 40, 64
+    t = T.from_numpy(tokens(n, vocab, 1)).cuda()
+    w, o = Strided(vocab, width, "f32", fill=np.ones((vocab, width), np.float32)), Strided(n, width, "f32")
+    need = lso.embed_grad_workspace_bytes(n, vocab, width)
+    ws = workspace(need)
+    e = _native.LsoEmbed(t.data_ptr(), n, w.t.data_ptr(), vocab, width, width, o.t.data_ptr(), width, 4, 1, 1, 0, 1.0)
+    m, b = Mats([(9, 30), (70, 90)], seed=1), Block([(9, 30), (70, 90)], "f32", False, seed=1)
+    mw = max(lso.orthogonalize_workspace_bytes(m.table), lso.muon_workspace_bytes(b.table))
+    mws = workspace(mw)
+    T.cuda.synchronize()
+    calls = [lambda: lib.lso_embed_lookup(ctypes.byref(e), None), lambda: lib.lso_embed_grad(ctypes.byref(e), ws.data_ptr(), need, None),
+             lambda: lib.lso_orthogonalize(m.table.ptr, 2, None, mws.data_ptr(), mw, None),
+             lambda: lib.lso_muon_step(b.table.ptr, 2, None, mws.data_ptr(), mw, None)]
+    log("calls beside an uncollected error")
+    for call in calls:
+        assert call() == 0               # (and the code objects are loaded)
+    lib.hipGetLastError()
+    seen = []
+    for call in calls:
+        left = lib.hipSetDevice(ctypes.c_int(1 << 20))    # no such device: a host-side refusal
+        status = call()
+        seen.append((left != 0, status, lib.hipGetLastError() == left, lib.hipGetLastError()))
+    T.cuda.synchronize()
+    assert seen == [(True, 0, True, 0)] * 4
