@@ -52,7 +52,7 @@ int small_class(uint64_t k, uint64_t side) { return k > side ? -1 : k <= 8 ? 0 :
 // singular values s, of s^2 and of the polynomial a + b s^2 + c s^4; and for
 // each step the power of two that the polynomial stays under, and whether it
 // and the next step's may be multiplied with each other (and with S).
-double most_value(const double* coef, uint32_t steps, uint32_t* shift, bool* pair)
+double most_value(const double* coef, uint32_t steps, int16_t* shift, bool* pair)
 {
     double s = 1.0, most = 1.0, poly_before = 0.0;
     bool alone = false;
@@ -65,8 +65,9 @@ double most_value(const double* coef, uint32_t steps, uint32_t* shift, bool* pai
         alone = !(poly * z <= kNsMostValue);
         poly_before = poly;
         pair[k] = false;
-        shift[k] = 0;
-        while (shift[k] < 4 && poly >= std::ldexp(1.0, static_cast<int>(shift[k]))) ++shift[k];
+        int above = 0;
+        if (poly > 0.0 && poly <= kNsMostValue) (void)std::frexp(poly, &above);
+        shift[k] = static_cast<int16_t>(std::max(above, -255));
         // s p(s^2) on [0, s]: at the end, and where 5 c t^2 + 3 b t + a = 0, t = s^2
         auto value = [&](double t) { return std::sqrt(t) * std::fabs(a + t * (b + t * c)); };
         double next = value(z);

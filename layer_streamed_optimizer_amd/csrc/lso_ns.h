@@ -129,7 +129,7 @@ struct NsCall {
     uint32_t steps;
     double eps;
     double coef[3 * kNsMaxSteps];
-    uint32_t shift[kNsMaxSteps];           // a step multiplies X by less than 2^shift
+    int16_t shift[kNsMaxSteps];            // a step multiplies X by less than 2^shift (-255 at least)
 };
 
 // Enqueue the table's upload to device_table and every launch (lso_ns.hip).

@@ -272,7 +272,8 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const NsMat* tab, uint32_t
 // (its scale is fixed), so the path works on X 2^e with e >= 0 chosen to
 // bring the norm of X_0 to [1/2, 2): with S' = S 2^2e the polynomial is
 // a + b 2^-2e S' + c 2^-4e S'^2, and each step lowers e by as many powers of
-// two as X can have grown by.
+// two as X can have grown by, or raises it by as many as X must have shrunk
+// by (five steps of 0.02 X would leave FP16's range as well).
 struct NsScaling {
     double inv;   // 2^e / (|u|_F + eps)
     int e;
@@ -542,10 +543,12 @@ struct ProductArgs {
     uint32_t a_square, b_square, out_square;   // which squares are read and written
     uint32_t depth;      // stages per part
     double ca, cb, cc;   // coefficients of the step (kPoly)
-    int lowered, lower;  // by how much the steps before and this one lower e
+    int16_t shift[kNsMaxSteps];   // each step's, as in NsCall
+    uint32_t step;
 };
 
-__device__ __forceinline__ int left_of(int e, int lowered) { return e > lowered ? e - lowered : 0; }
+// e behind a step; it stays at 0 or above.
+__device__ __forceinline__ int step_scale(int e, int shift) { return e > shift ? e - shift : 0; }
 
 // Tile number k of the tiles on and under the diagonal of tm x tm, in bands
 // of four rows, down the columns of a band: tiles near each other in this
@@ -786,8 +789,14 @@ __global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(co
     // square), kStrip rows at a time
     float unscale = 1.0f / kNsScale, ca = 0.0f, cb = 0.0f, cc = 0.0f;
     if (kKind == kPoly || kKind == kLast) {
-        const int e0 = reinterpret_cast<const NsScaling*>(m.work + w.inv)->e;
-        const int before = left_of(e0, args.lowered), after = left_of(e0, args.lowered + args.lower), up = after - before;
+        int before = reinterpret_cast<const NsScaling*>(m.work + w.inv)->e, after = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < kNsMaxSteps; ++k) {
+            if (k > args.step) break;
+            if (k == args.step) after = step_scale(before, args.shift[k]);
+            else before = step_scale(before, args.shift[k]);
+        }
+        const int up = after - before;
         if (kKind == kLast) unscale = ldexpf(1.0f / (kNsScale * kNsScale), -after);
         ca = static_cast<float>(ldexp(args.ca, up));
         cb = static_cast<float>(ldexp(args.cb, up - 2 * before));
@@ -1225,6 +1234,7 @@ public:
         args_.counters = c.counters;
         args_.n = c.nbig;
         args_.layout = c.layout;
+        for (uint32_t k = 0; k < kNsMaxSteps; ++k) args_.shift[k] = c.shift[k];
     }
 
     hipError_t run()
@@ -1296,9 +1306,7 @@ private:
         args_.ca = c_.coef[3 * k];
         args_.cb = c_.coef[3 * k + 1];
         args_.cc = c_.coef[3 * k + 2];
-        args_.lowered = 0;
-        for (uint32_t j = 0; j < k; ++j) args_.lowered += static_cast<int>(c_.shift[j]);
-        args_.lower = static_cast<int>(c_.shift[k]);
+        args_.step = k;
         if (!two_term_squares()) launch<1, 1, kPoly, 1>(c_.square);
         else if (multiplier) launch<2, 2, kPoly, kTerms>(c_.square);
         else launch<2, 2, kPoly, 2>(c_.square);

@@ -614,3 +614,21 @@ def test_tables_take_type_and_stride_from_tensors():
     log("update from tensors")
     run_muon(b)
     b.check(what="from tensors")
+
+
+@pytest.mark.parametrize("precision", [lso.LSO_NS_FULL, lso.LSO_NS_HALF])
+def test_orthogonalize_with_coefficients_that_shrink(precision):
+    """Steps that make X small, alone and before and between others: X keeps
+    its bits (its operands are scaled), so errors stay those of any step.  A
+    linear step is off by its operands' rounding alone, less than the default
+    ones that the tolerance is made for."""
+    shapes = [(40, 60), (100, 130), (130, 100), (90, 3000), (1500, 80)]     # the small path, single steps, pairs
+    default, tiny, mild = COEF, (0.02, 0.0, 0.0), (0.3, -0.1, 0.0)
+    for coef in ([tiny] * 5, [tiny, default, default, default], [default, default, tiny, tiny, default], [mild] * 16, [(1e-30, 0.0, 0.0)],
+                 [tiny, (1.5, -0.5, 0.0)] * 3, [(0.0, 0.0, 0.0)] * 2):
+        m = Mats(shapes, seed=33)
+        log(f"orthogonalize with coefficients that shrink, precision {precision}, {coef}")
+        for (r, c), src, got in zip(shapes, m.src, run_ortho(m, steps=len(coef), coefficients=coef, precision=precision)):
+            want = ortho64(src, len(coef), coef=coef)
+            norm = np.linalg.norm(want)
+            assert np.linalg.norm(got - want) <= tolerance(r, c, precision == lso.LSO_NS_FULL, False) * norm, (r, c, coef)
