@@ -1,8 +1,9 @@
 // Newton-Schulz orthogonalisation and the orthogonalised-momentum update for
 // gfx950.  Formulas and precisions: lso_ops.h.
 //
-// General path (smaller side above 64), all matrices of a call together, one
-// launch per step below:
+// General path (smaller side above 64, or above 32 where a few of those come
+// with larger matrices), all matrices of a call together, one launch per step
+// below:
 //   norm     u (for the update: m' and u), its sum of squares per tile
 //   scale    1 / (|u|_F + eps) per matrix
 //   split    X_0 = u / (|u|_F + eps) into FP16 operands, X and its transpose

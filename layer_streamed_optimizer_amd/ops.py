@@ -306,8 +306,10 @@ def embed_grad_workspace_bytes(n_tokens: int, vocab: int, width: int) -> int:
 
 def embed_grad(tokens, dy, grad, workspace, workspace_bytes: int, *, scale: float = 1.0, accumulate: bool = False,
                stream=None) -> None:
-    """grad[v] = scale * sum of dy[i] over the positions i of token v (+= with
-    accumulate), every row of grad written.  Torch tensors; asynchronous."""
+    """grad[v] = scale * sum of dy[i] over the positions i of token v; every row
+    of grad is written, zeros where a token does not occur.  With accumulate,
+    += that, and such rows are left as they are.  Torch tensors;
+    asynchronous."""
     e = _embed(tokens, grad, dy, scale, LSO_EMBED_ADD if accumulate else 0)
     st = _native.lib().lso_embed_grad(ctypes.byref(e), _workspace(workspace, workspace_bytes), int(workspace_bytes), stream_handle(stream))
     if st:
