@@ -426,3 +426,73 @@ def test_an_error_left_by_other_work_stays_there():
         seen.append((left != 0, status, lib.hipGetLastError() == left, lib.hipGetLastError()))
     T.cuda.synchronize()
     assert seen == [(True, 0, True, 0)] * 4
+
+
+L2_BYTES = 32 << 20      # rows of more than this are read, or written, past the caches
+
+
+def grad_on_device(t, dy, vocab, scale, old):
+    """grad_reference on the device: (value, sum of sizes, count) in 64 bits."""
+    T = torch()
+    real = (t >= 0) & (t < vocab)
+    ids, rows = t[real].long(), dy[real].double()
+    out = T.zeros(vocab, dy.shape[1], dtype=T.float64, device="cuda")
+    size, count = T.zeros_like(out), T.bincount(ids, minlength=vocab).double()
+    out.index_add_(0, ids, rows)
+    size.index_add_(0, ids, rows.abs())
+    s = float(np.float32(scale))
+    out, size = out * s, size * abs(s)
+    if old is not None:
+        out, size = out + old, size + old.abs()
+    return out, size, count
+
+
+@pytest.mark.parametrize("n,vocab,width,pad,kind", [(20000, 3000, 1024, 0, "zipf"), (9000, 20000, 2048, 8, "zipf"),
+                                                    (33000, 32000, 520, 0, "ramp"), (40000, 17, 424, 0, "ramp"), (17000, 2, 1032, 0, "same")])
+@pytest.mark.parametrize("dy_dt,grad_dt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+def test_gradient_of_rows_beyond_the_caches(n, vocab, width, pad, kind, dy_dt, grad_dt):
+    """Long and short runs, padding and empty rows among them."""
+    T = torch()
+    assert n * width * (2 if dy_dt == "bf16" else 4) > L2_BYTES and width % 8 == 0 and pad % 8 == 0
+    T.manual_seed(n)
+    t = T.from_numpy(tokens(n, vocab, n + 2, kind))
+    if kind != "zipf":
+        t[::9] = -1
+    t = t.cuda()
+    dy = Strided(n, width, dy_dt, pad)
+    dy.t.copy_(T.randn(n, width, device="cuda"))
+    need = lso.embed_grad_workspace_bytes(n, vocab, width)
+    for accumulate in (False, True):
+        grad = Strided(vocab, width, grad_dt, pad)
+        if accumulate:
+            grad.t.copy_(T.randn(vocab, width, device="cuda"))
+        before = grad.t.clone()
+        ws = workspace(need)
+        log(f"grad beyond the caches n {n} vocab {vocab} width {width} pad {pad} {kind} {dy_dt}->{grad_dt} add {accumulate}")
+        lso.embed_grad(t.int() if accumulate else t, dy.t, grad.t, ws, need, scale=0.75, accumulate=accumulate)
+        T.cuda.synchronize()
+        assert bool((ws[need:] == 0xFF).all()), "written behind the workspace"
+        grad.check_canaries()
+        want, size, count = grad_on_device(t, dy.t, vocab, 0.75, before.double() if accumulate else None)
+        tol = (count[:, None] + 3) * 2.0**-24 * size + rounding(grad_dt) * want.abs()
+        assert bool(((grad.t.double() - want).abs() <= tol).all())
+        empty = count == 0
+        assert T.equal(grad.t[empty], before[empty]) if accumulate else not bool(grad.t[empty].any())
+
+
+@pytest.mark.parametrize("table", ["bf16", "f32"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_lookup_of_rows_beyond_the_caches(table, out):
+    T = torch()
+    n, vocab, width = 20000, 3000, 1032
+    assert n * width * (2 if out == "bf16" else 4) > L2_BYTES
+    t = T.from_numpy(tokens(n, vocab, 4)).cuda()
+    w, o = Strided(vocab, width, table, 8), Strided(n, width, out, 8)
+    w.t.copy_(T.randn(vocab, width, device="cuda"))
+    log(f"lookup beyond the caches {table}->{out}")
+    lso.embed_lookup(t, w.t, o.t, scale=1.7)
+    T.cuda.synchronize()
+    real = (t >= 0) & (t < vocab)
+    want = T.where(real[:, None], w.t.double()[t.clamp(0, vocab - 1)] * float(np.float32(1.7)), 0.0)
+    assert bool(((o.t.double() - want).abs() <= (2.0**-24 + rounding(out)) * want.abs()).all())
+    o.check_canaries()
