@@ -679,8 +679,8 @@ __global__ void __launch_bounds__(kT == 256 ? 512 : 256, 2) ns_product_kernel(co
     };
     // Multiply what has been read; in between, while the matrix cores are
     // busy, send for stage s.  Sent for beside the reads of LDS, the loads held
-    // those up: the matrix cores were busy 58% of the time against 78% now,
-    // the product of 8192 x 8192 and 8192 x 28672 took 10.0 against 8.6 ms.
+    // those up: the matrix cores were busy 58% of the time against 80% now,
+    // the product of 8192 x 8192 and 8192 x 28672 took 10.0 against 8.7 ms.
     auto multiply = [&](uint32_t s, bool send) {
         product(fa[0], fb[0]);
         __builtin_amdgcn_sched_barrier(0);
