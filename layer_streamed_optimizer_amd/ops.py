@@ -41,9 +41,10 @@ def dtype_of(tensor) -> int:
 def _array(x, name: str, code: int | None, default: int, rows: int, cols: int, ld: int | None = None) -> tuple:
     """(address, LSO_DT_* code, row stride) of a matrix's array.  An address
     has the type and stride that are given, or `default` and cols.  A torch
-    tensor of shape [rows, cols] brings both; any contiguous one that holds
-    them may stand for the rows at stride ld, and one of integers of the same
-    size for their bits.  What contradicts the tensor is refused."""
+    tensor of shape [rows, cols] brings both; a contiguous one of shape
+    [rows, ld], or of one or more than two dimensions, that holds them may
+    stand for the rows at stride ld, and one of integers of the same size for
+    their bits.  What contradicts the tensor is refused."""
     if x is None or isinstance(x, int):
         return x or 0, default if code is None else code, cols if ld is None else ld
     addr, dtype = x.data_ptr(), x.dtype
@@ -65,7 +66,8 @@ def _array(x, name: str, code: int | None, default: int, rows: int, cols: int, l
             if ld is not None and ld != in_rows:
                 raise ValueError(f"{name}: row stride {ld} given for a tensor of row stride {in_rows}")
             ld = in_rows
-    elif not x.is_contiguous() or x.numel() < (rows - 1) * (cols if ld is None else ld) + cols:
+    elif (not x.is_contiguous() or x.numel() < (rows - 1) * (cols if ld is None else ld) + cols
+          or x.dim() == 2 and x.shape != (rows, ld)):
         raise ValueError(f"{name}: a tensor of shape {tuple(x.shape)} and strides {x.stride()} does not hold {rows} x {cols}")
     return addr, own, cols if ld is None else ld
 

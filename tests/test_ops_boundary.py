@@ -377,3 +377,16 @@ def test_embedding_producer_waits_for_its_tensors(monkeypatch):
     assert seen == [2]
     p.set_batch(t, dy)
     assert seen == [2, 2]
+
+
+def test_matrix_tables_refuse_tensors_of_another_shape():
+    """A matrix given with its sides exchanged is not read as another one."""
+    import torch
+    for x, kw in ((torch.zeros(10, 6), {}), (torch.zeros(10, 6), dict(ld_x=10)), (torch.zeros(5, 12), {}), (torch.zeros(1, 60), {}),
+                  (torch.zeros(6, 12), dict(ld_x=11))):
+        with pytest.raises(ValueError, match="does not hold 6 x 10"):
+            lso.MatrixTable.from_rows([dict(x=x, y=A, rows=6, cols=10, **kw)])
+    with pytest.raises(ValueError, match="grad: .* does not hold 64 x 96"):
+        lso.MuonTable.from_rows([block(grad=torch.zeros(96, 64))])
+    for x, kw in ((torch.zeros(6, 12), dict(ld=12)), (torch.zeros(60), {}), (torch.zeros(6, 5, 2), {})):
+        assert ops._array(x, "x", None, 2, 6, 10, **kw) == (x.data_ptr(), 1, kw.get("ld", 10))
