@@ -3,7 +3,8 @@ layer-streamed from host memory or files.
 
 A thin binding over liblso.so (include/lso.h): it marshals descriptor tables
 and stream handles; every step of the update runs in the HIP library.
-PyTorch, where used, only provides device memory and streams.
+PyTorch, where used, only provides device memory and streams; import it
+before the first call here, so that both load one HIP runtime.
 
     table = BlockTable.from_rows([...])       # one dict per block
     table.set_step(t)                         # the caller owns t
